@@ -29,7 +29,8 @@ EXPORTS = (
     "prism_attn_workspace_size", "prism_attn_fwd", "prism_attn_bwd", "prism_workspace_status",
     "prism_last_error", "prism_version", "prism_kernel_launches", "prism_plan_noalloc",
     "prism_kernel_timing", "prism_kernel_timing_read", "prism_a2v_norm", "prism_diag_exp2",
-    "prism_diag_wait_timeout", "prism_project_v_plan",
+    "prism_diag_wait_timeout", "prism_project_v_plan", "prism_ckpt8_pack", "prism_ckpt8_unpack",
+    "prism_linear_workspace_size", "prism_linear_fwd", "prism_linear_bwd",
 )
 KERNEL_TIMING_IDS = 25  # PRISM_KERNEL_TIMING_IDS in include/prism.h
 
@@ -49,6 +50,14 @@ class PrismPlan(C.Structure):
 class PrismSelect(C.Structure):
     _fields_ = [("row_ptr", C.c_void_p), ("col", C.c_void_p), ("cap", C.c_int64), ("nnz", C.c_int64),
                 ("col_ptr", C.c_void_p), ("row", C.c_void_p)]
+
+
+class PrismCkpt8(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scales", C.c_void_p), ("ld", C.c_int64)]
+
+
+class PrismLinear(C.Structure):
+    _fields_ = [("n", C.c_int64), ("in_", C.c_int32), ("out", C.c_int32), ("act", C.c_int32)]
 
 
 class PrismError(RuntimeError):
@@ -93,6 +102,13 @@ def load() -> C.CDLL:
         "prism_diag_exp2": (C.c_int, [vp, vp, vp, C.c_int64, st]),
         "prism_diag_wait_timeout": (C.c_int, [vp, sz, C.c_int64, st]),
         "prism_project_v_plan": (C.c_int, [P(PrismParams), vp, C.c_int32, vp, vp, vp, P(PrismPlan), vp, sz, st]),
+        "prism_ckpt8_pack": (C.c_int, [vp, C.c_int64, C.c_int32, C.c_int64, P(PrismCkpt8), st]),
+        "prism_ckpt8_unpack": (C.c_int, [P(PrismCkpt8), C.c_int64, C.c_int32, vp, C.c_int64, st]),
+        "prism_linear_workspace_size": (sz, [P(PrismLinear), C.c_int]),
+        "prism_linear_fwd": (C.c_int, [P(PrismLinear), vp, C.c_int64, vp, vp, vp, C.c_int64, vp, C.c_int64, vp,
+                                       P(PrismCkpt8), vp, sz, st]),
+        "prism_linear_bwd": (C.c_int, [P(PrismLinear), vp, C.c_int64, vp, C.c_int64, P(PrismCkpt8), vp, vp, C.c_int64,
+                                       P(PrismCkpt8), vp, vp, vp, C.c_int, vp, sz, st]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

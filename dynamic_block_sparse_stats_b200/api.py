@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import PrismParams, PrismPlan, PrismSelect, check
+from ._lib import PrismCkpt8, PrismLinear, PrismParams, PrismPlan, PrismSelect, check
 
 
 # guidance bits and density modes of the ablation variants (include/prism.h)
@@ -412,3 +412,240 @@ def workspace_status(ws: torch.Tensor, stream=None) -> int:
     dev = _check_devices([("ws", ws)])
     with torch.cuda.device(dev):
         return _lib.load().prism_workspace_status(_ptr(ws), _stream(stream, dev))
+
+
+# ----------------------------------------------------------------------------- 8-bit activation checkpoints
+@dataclass
+class Ckpt8:
+    """An activation [n, width] held in 8 bits (prism_ckpt8_t): codes i8
+    [n, ld] and scales u8 [n, ld / 32], ld = width rounded up to a multiple of
+    128; a value is code * 2^(scale - 127)."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    width: int
+
+    def c_struct(self) -> PrismCkpt8:
+        return PrismCkpt8(self.codes.data_ptr(), self.scales.data_ptr(), self.codes.shape[1])
+
+
+def alloc_ckpt8(n: int, width: int, device) -> Ckpt8:
+    ld = (width + 127) // 128 * 128
+    return Ckpt8(torch.empty((n, ld), dtype=torch.int8, device=device),
+                 torch.empty((n, ld // 32), dtype=torch.uint8, device=device), width)
+
+
+def _check_ckpt8(c, name, n, width):
+    if not isinstance(c, Ckpt8):
+        raise TypeError(f"{name} must be an api.Ckpt8, got {type(c).__name__}")
+    if c.width != width:
+        raise ValueError(f"{name} holds {c.width} channels, the call needs {width}")
+    ld = (width + 127) // 128 * 128
+    _check_tensor(c.codes, name + ".codes", torch.int8, (n, ld))
+    _check_tensor(c.scales, name + ".scales", torch.uint8, (n, ld // 32))
+    return [(name + ".codes", c.codes), (name + ".scales", c.scales)]
+
+
+def _check_rows(t, name, shape=None):
+    """A 2-D bf16 tensor whose rows may be strided (contiguous within a row);
+    returns its row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        want = "two dimensions" if shape is None else f"shape {tuple(shape)}"
+        raise ValueError(f"{name} must have {want}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    if t.shape[0] <= 1:
+        return t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} rows overlap (stride {t.stride(0)}, {t.shape[1]} channels)")
+    return t.stride(0)
+
+
+def ckpt8_pack(x: torch.Tensor, out: Ckpt8 | None = None, stream=None) -> Ckpt8:
+    """prism_ckpt8_pack: the 8-bit checkpoint of a bf16 activation x [n, width]
+    (rows may be strided; width a multiple of 8)."""
+    ld = _check_rows(x, "x")
+    n, width = x.shape
+    named = [("x", x)] + (_check_ckpt8(out, "out", n, width) if out is not None else [])
+    dev = _check_devices(named)
+    with torch.cuda.device(dev):
+        out = out if out is not None else alloc_ckpt8(n, width, dev)
+        cs = out.c_struct()
+        check(_lib.load().prism_ckpt8_pack(_ptr(x), n, width, ld, C.byref(cs), _stream(stream, dev)))
+    return out
+
+
+def ckpt8_unpack(c: Ckpt8, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """prism_ckpt8_unpack: the activation a checkpoint holds, bf16 [n, width]
+    (into `out`, whose rows may be strided)."""
+    if not isinstance(c, Ckpt8) or not isinstance(c.codes, torch.Tensor) or c.codes.dim() != 2:
+        raise TypeError("c must be an api.Ckpt8")
+    n = c.codes.shape[0]
+    named = _check_ckpt8(c, "c", n, c.width)
+    ld = c.width
+    if out is not None:
+        ld = _check_rows(out, "out", (n, c.width))
+        named.append(("out", out))
+    dev = _check_devices(named)
+    with torch.cuda.device(dev):
+        out = out if out is not None else torch.empty((n, c.width), dtype=torch.bfloat16, device=dev)
+        cs = c.c_struct()
+        check(_lib.load().prism_ckpt8_unpack(C.byref(cs), n, c.width, _ptr(out), ld, _stream(stream, dev)))
+    return out
+
+
+# ----------------------------------------------------------------------------- linear maps
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3  # activations of the linear map (gelu: tanh form)
+
+
+@dataclass
+class LinearResult:
+    """Output of prism_linear_fwd: Y bf16 [n, out]; Z the saved
+    pre-activation (bf16 tensor, Ckpt8 or None); ws the call's workspace
+    (its status word says whether a kernel gave up on a wait)."""
+    Y: torch.Tensor
+    Z: torch.Tensor | Ckpt8 | None
+    ws: torch.Tensor
+
+
+@dataclass
+class LinearGrads:
+    """Output of prism_linear_bwd: dX bf16 [n, in], dW [out, in], db [out]
+    (bf16 or fp32; None where not asked for), ws the call's workspace."""
+    dX: torch.Tensor | None
+    dW: torch.Tensor | None
+    db: torch.Tensor | None
+    ws: torch.Tensor
+
+
+def linear_workspace_size(n: int, cin: int, cout: int, act: int = ACT_NONE, backward: bool = False) -> int:
+    """Bytes of the `ws` buffer linear_fwd / linear_bwd takes for n tokens."""
+    size = _lib.load().prism_linear_workspace_size(C.byref(PrismLinear(n, cin, cout, act)), int(backward))
+    if size == 0:
+        raise _lib.PrismError(_lib.PRISM_ERR_INVALID_ARG, _lib.load().prism_last_error().decode(errors="replace"))
+    return size
+
+
+def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = None, act: int = ACT_NONE,
+               residual: torch.Tensor | None = None, save: str | None = None, Y: torch.Tensor | None = None,
+               Z: torch.Tensor | Ckpt8 | None = None, ws: torch.Tensor | None = None, stream=None) -> LinearResult:
+    """prism_linear_fwd: Y = act(X W^T + bias) + residual.  X bf16 [n, in], W
+    bf16 [out, in], bias bf16 [out], residual bf16 [n, out]; X, residual and Y
+    rows may be strided.  save = "bf16" or "ckpt8" keeps the pre-activation for
+    linear_bwd (into Z when given)."""
+    ldx = _check_rows(X, "X")
+    n, cin = X.shape
+    if not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("W must be a 2-D tensor [out, in]")
+    cout = W.shape[0]
+    _check_tensor(W, "W", torch.bfloat16, (cout, cin))
+    named = [("X", X), ("W", W), ("bias", bias), ("residual", residual), ("Y", Y), ("ws", ws)]
+    if bias is not None:
+        _check_tensor(bias, "bias", torch.bfloat16, (cout,))
+    ldr = _check_rows(residual, "residual", (n, cout)) if residual is not None else 0
+    ldy = _check_rows(Y, "Y", (n, cout)) if Y is not None else cout
+    if save not in (None, "bf16", "ckpt8"):
+        raise ValueError(f'save must be None, "bf16" or "ckpt8", got {save!r}')
+    if Z is not None:
+        if save is None:
+            raise ValueError("Z is given but save is None")
+        if save == "bf16":
+            _check_tensor(Z, "Z", torch.bfloat16, (n, cout))
+            named.append(("Z", Z))
+        else:
+            named += _check_ckpt8(Z, "Z", n, cout)
+    if ws is not None:
+        _check_workspace(ws, "ws")
+    dev = _check_devices(named)
+    lib = _lib.load()
+    with torch.cuda.device(dev):
+        Y = Y if Y is not None else torch.empty((n, cout), dtype=torch.bfloat16, device=dev)
+        if Z is None and save is not None:
+            Z = torch.empty_like(Y, memory_format=torch.contiguous_format) if save == "bf16" else \
+                alloc_ckpt8(n, cout, dev)
+        l = PrismLinear(n, cin, cout, act)
+        ws = ws if ws is not None else _workspace(lib.prism_linear_workspace_size(C.byref(l), 0), dev)
+        z8 = Z.c_struct() if save == "ckpt8" else None
+        check(lib.prism_linear_fwd(C.byref(l), _ptr(X), ldx, _ptr(W), _ptr(bias), _ptr(residual), ldr, _ptr(Y), ldy,
+                                   _ptr(Z) if save == "bf16" else None, C.byref(z8) if z8 is not None else None,
+                                   _ptr(ws), ws.numel(), _stream(stream, dev)))
+    return LinearResult(Y, Z, ws)
+
+
+def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor | None,
+               Z: torch.Tensor | Ckpt8 | None = None, act: int = ACT_NONE, need=("dX", "dW", "db"),
+               grad_fp32: bool = False, out=None, ws: torch.Tensor | None = None, stream=None) -> LinearGrads:
+    """prism_linear_bwd: the gradients named in `need` of linear_fwd, from dY
+    bf16 [n, out], the forward's X [n, in] (bf16 or a Ckpt8; needed for dW), W
+    (needed for dX) and, with an activation, the saved pre-activation Z (bf16 or
+    a Ckpt8).  dX is bf16; dW and db bf16, or fp32 with grad_fp32.  `out` may
+    hold (dX, dW, db) buffers, None entries allocated.  The residual's gradient
+    is dY itself."""
+    lddy = _check_rows(dY, "dY")
+    n, cout = dY.shape
+    need = tuple(need)
+    if not need or any(k not in ("dX", "dW", "db") for k in need):
+        raise ValueError(f'need must name some of "dX", "dW", "db", got {need!r}')
+    if "dX" in need and W is None:
+        raise ValueError("dX needs W")
+    if "dW" in need and X is None:
+        raise ValueError("dW needs X")
+    if W is not None:
+        if not isinstance(W, torch.Tensor) or W.dim() != 2:
+            raise ValueError("W must be a 2-D tensor [out, in]")
+        cin = W.shape[1]
+        _check_tensor(W, "W", torch.bfloat16, (cout, cin))
+    elif X is not None:
+        cin = X.width if isinstance(X, Ckpt8) else X.shape[-1]
+    else:
+        cin = 8  # only db: the input's width does not matter
+    named = [("dY", dY), ("W", W)]
+    ldx = ldz = 0
+    if isinstance(X, Ckpt8):
+        named += _check_ckpt8(X, "X", n, cin)
+    elif X is not None:
+        ldx = _check_rows(X, "X", (n, cin))
+        named.append(("X", X))
+    if act == ACT_NONE:
+        Z = None
+    elif isinstance(Z, Ckpt8):
+        named += _check_ckpt8(Z, "Z", n, cout)
+    elif Z is None:
+        raise ValueError("the activation's gradient needs Z")
+    else:
+        ldz = _check_rows(Z, "Z", (n, cout))
+        named.append(("Z", Z))
+    dt = torch.float32 if grad_fp32 else torch.bfloat16
+    want = {"dX": ((n, cin), torch.bfloat16), "dW": ((cout, cin), dt), "db": ((cout,), dt)}
+    if out is None:
+        out = (None, None, None)
+    if len(out) != 3:
+        raise ValueError("out must hold three entries (dX, dW, db)")
+    for name, t in zip(("dX", "dW", "db"), out):
+        if t is not None:
+            if name not in need:
+                raise ValueError(f"out holds {name}, which need does not name")
+            _check_tensor(t, name, want[name][1], want[name][0])
+            named.append((name, t))
+    if ws is not None:
+        _check_workspace(ws, "ws")
+        named.append(("ws", ws))
+    dev = _check_devices(named)
+    lib = _lib.load()
+    with torch.cuda.device(dev):
+        dX, dW, db = (None if name not in need else
+                      t if t is not None else torch.empty(want[name][0], dtype=want[name][1], device=dev)
+                      for name, t in zip(("dX", "dW", "db"), out))
+        l = PrismLinear(n, cin, cout, act)
+        ws = ws if ws is not None else _workspace(lib.prism_linear_workspace_size(C.byref(l), 1), dev)
+        x8 = X.c_struct() if isinstance(X, Ckpt8) else None
+        z8 = Z.c_struct() if isinstance(Z, Ckpt8) else None
+        check(lib.prism_linear_bwd(C.byref(l), _ptr(dY), lddy, None if x8 is not None else _ptr(X), ldx,
+                                   C.byref(x8) if x8 is not None else None, _ptr(W),
+                                   None if z8 is not None else _ptr(Z), ldz,
+                                   C.byref(z8) if z8 is not None else None, _ptr(dX), _ptr(dW), _ptr(db),
+                                   int(bool(grad_fp32)), _ptr(ws), ws.numel(), _stream(stream, dev)))
+    return LinearGrads(dX, dW, db, ws)

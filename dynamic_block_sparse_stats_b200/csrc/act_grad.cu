@@ -1,0 +1,234 @@
+// First pass of prism_linear_bwd: dZ = dY * act'(Z), rounded to bf16 for the two
+// matrix products that follow, and the bias gradient db = column sums of dZ
+// (taken from the fp32 values before that rounding).
+//
+// HBM-bound: dY and Z (bf16, or an 8-bit checkpoint) are read once, dZ written
+// once.  A thread owns eight columns (one 16-byte vector) of every k-th row of
+// its block, so its eight fp32 column sums stay in registers; the block's row
+// lanes meet in shared memory, the blocks in a second kernel, all in a fixed
+// order.  Without an activation dZ is dY itself and only the sums are taken.
+#include <algorithm>
+
+#include "ckpt8.cuh"
+#include "internal.h"
+
+namespace prism {
+namespace actg {
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+
+// act'(z) in fp32, with p = 1 / (1 + e^-v).
+//   silu = z p(z):             slope p (1 + z (1 - p))
+//   gelu (tanh form) = z p(v), v = 2 sqrt(2/pi) (z + 0.044715 z^3): slope
+//                              p + z p (1 - p) v'
+// z is clamped where p is 0 or 1 to the last bit (e^-v overflows or vanishes), so
+// that no product of infinity and zero arises.  A NaN stays one (a restored
+// checkpoint block that held a non-finite value).
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == PRISM_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+  constexpr float kFar = ACT == PRISM_ACT_SILU ? 100.f : 30.f;
+  const float c = fminf(fmaxf(z, -kFar), kFar);
+  float s;
+  if constexpr (ACT == PRISM_ACT_SILU) {
+    const float p = __fdividef(1.f, 1.f + __expf(-c));
+    s = p * fmaf(c, 1.f - p, 1.f);
+  } else {
+    const float z2 = c * c;
+    const float p = __fdividef(1.f, 1.f + __expf(-1.5957691216057308f * fmaf(0.044715f * z2, c, c)));
+    s = fmaf(c * p * (1.f - p), 1.5957691216057308f * fmaf(0.134145f, z2, 1.f), p);
+  }
+  return z != z ? z : s;
+}
+
+struct Src {
+  const uint4 *dY;
+  long long ldy_vec;
+  const uint4 *Z;  // bf16, or NULL
+  long long ldz_vec;
+  const uint2 *codes;  // checkpoint, or NULL
+  const uint8_t *scales;
+  long long ldq;
+  uint4 *dZ;  // [n][cols]
+};
+
+// tx threads (a power of two, 8..32) cover 8 * tx columns of a row
+template <int ACT, bool Z8>
+__global__ void __launch_bounds__(kThreads)
+    act_grad_kernel(const Src s, long long n, int vecs, int tx, long long rows_per, float *__restrict__ part) {
+  __shared__ float red[kThreads][9];
+  const int cx = threadIdx.x & (tx - 1), ry = threadIdx.x / tx, rows_step = kThreads / tx;
+  const int cv = blockIdx.x * tx + cx;
+  const long long r0 = (long long)blockIdx.y * rows_per;
+  const long long r1 = r0 + rows_per < n ? r0 + rows_per : n;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (cv < vecs) {
+    for (long long r = r0 + ry; r < r1; r += (long long)rows_step * kUnroll) {
+      uint4 d[kUnroll], z[kUnroll];
+      uint32_t sc[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const long long rr = r + (long long)u * rows_step;
+        if (rr < r1) {
+          d[u] = ACT != PRISM_ACT_NONE ? __ldcs(s.dY + rr * s.ldy_vec + cv) : __ldg(s.dY + rr * s.ldy_vec + cv);
+          if constexpr (ACT != PRISM_ACT_NONE) {
+            if constexpr (Z8) {
+              const uint2 q = __ldcs(s.codes + rr * (s.ldq >> 3) + cv);
+              z[u].x = q.x;
+              z[u].y = q.y;
+              sc[u] = __ldg(s.scales + rr * (s.ldq >> 5) + (cv >> 2));
+            } else {
+              z[u] = __ldcs(s.Z + rr * s.ldz_vec + cv);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const long long rr = r + (long long)u * rows_step;
+        if (rr >= r1) break;
+        const uint32_t dw[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
+        if constexpr (ACT != PRISM_ACT_NONE) {
+          uint4 zz = z[u];
+          if constexpr (Z8) {
+            const uint32_t s2 = ckpt8_scale2(sc[u]);
+            zz = make_uint4(ckpt8_restore2(z[u].x, 0x4140, s2), ckpt8_restore2(z[u].x, 0x4342, s2),
+                            ckpt8_restore2(z[u].y, 0x4140, s2), ckpt8_restore2(z[u].y, 0x4342, s2));
+          }
+          const uint32_t zw[4] = {zz.x, zz.y, zz.z, zz.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float lo = bf16lo(dw[k]) * act_slope<ACT>(bf16lo(zw[k]));
+            const float hi = bf16hi(dw[k]) * act_slope<ACT>(bf16hi(zw[k]));
+            sum[2 * k] += lo;
+            sum[2 * k + 1] += hi;
+            o[k] = pack_bf16(lo, hi);
+          }
+          s.dZ[rr * vecs + cv] = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            sum[2 * k] += bf16lo(dw[k]);
+            sum[2 * k + 1] += bf16hi(dw[k]);
+          }
+        }
+      }
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) red[threadIdx.x][k] = sum[k];
+  __syncthreads();
+  // 8 * tx columns, summed over the row lanes
+  for (int c = threadIdx.x; c < 8 * tx; c += kThreads) {
+    if (blockIdx.x * tx + (c >> 3) < vecs) {
+      float a = 0.f;
+      for (int y = 0; y < rows_step; ++y) a += red[y * tx + (c >> 3)][c & 7];
+      part[(long long)blockIdx.y * vecs * 8 + (long long)blockIdx.x * tx * 8 + c] = a;
+    }
+  }
+}
+
+// db[c] = sum over the blocks: 32 columns per CTA, 8 lanes of blocks each
+__global__ void __launch_bounds__(256)
+    bias_grad_kernel(const float *__restrict__ part, int blocks, int cols, void *__restrict__ db, int fp32) {
+  __shared__ float red[8][33];
+  const int cx = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + cx;
+  float a = 0.f;
+  if (c < cols)
+    for (int b = y; b < blocks; b += 8) a += part[(long long)b * cols + c];
+  red[y][cx] = a;
+  __syncthreads();
+  if (y == 0 && c < cols) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) a += red[k][cx];
+    if (fp32)
+      static_cast<float *>(db)[c] = a;
+    else
+      static_cast<uint16_t *>(db)[c] = (uint16_t)(pack_bf16(a, a) & 0xffffu);
+  }
+}
+
+struct Shape {
+  int tx, strips, blocks;
+  long long rows_per;
+};
+// row blocks: enough CTAs for every SM's 8, each thread at least one full
+// unrolled step of rows
+static Shape shape_of(long long n, int cols) {
+  Shape s;
+  const int vecs = cols / 8;
+  s.tx = vecs >= 32 ? 32 : vecs >= 16 ? 16 : 8;
+  s.strips = (vecs + s.tx - 1) / s.tx;
+  const long long step = (long long)(kThreads / s.tx) * kUnroll;
+  const long long most = std::max<long long>(1, (long long)device_sm_count() * 8 / s.strips);
+  const long long want = std::max<long long>(1, std::min(most, (n + step - 1) / step));
+  s.rows_per = std::max<long long>(1, (n + want - 1) / want);
+  s.blocks = (int)std::max<long long>(1, (n + s.rows_per - 1) / s.rows_per);
+  return s;
+}
+
+struct Launch {
+  Src s;
+  dim3 grid;
+  long long n;
+  int vecs, tx;
+  long long rows_per;
+  float *part;
+  cudaStream_t st;
+};
+template <int ACT>
+static void run(const Launch &l, bool z8) {
+  if (z8)
+    act_grad_kernel<ACT, true><<<l.grid, kThreads, 0, l.st>>>(l.s, l.n, l.vecs, l.tx, l.rows_per, l.part);
+  else
+    act_grad_kernel<ACT, false><<<l.grid, kThreads, 0, l.st>>>(l.s, l.n, l.vecs, l.tx, l.rows_per, l.part);
+}
+
+}  // namespace actg
+
+size_t act_grad_part_bytes(long long n, int cols) {
+  return align_up(sizeof(float) * (size_t)actg::shape_of(n, cols).blocks * cols, 256);
+}
+
+cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, long long ldy, const uint16_t *Z,
+                            long long ldz, const prism_ckpt8_t *Z8, uint16_t *dZ, float *part, void *db, int db_fp32,
+                            cudaStream_t st) {
+  const actg::Shape sh = actg::shape_of(n, cols);
+  actg::Src s;
+  s.dY = reinterpret_cast<const uint4 *>(dY);
+  s.ldy_vec = ldy / 8;
+  s.Z = reinterpret_cast<const uint4 *>(Z);
+  s.ldz_vec = ldz / 8;
+  s.codes = Z8 ? reinterpret_cast<const uint2 *>(Z8->codes) : nullptr;
+  s.scales = Z8 ? Z8->scales : nullptr;
+  s.ldq = Z8 ? Z8->ld : 0;
+  s.dZ = reinterpret_cast<uint4 *>(dZ);
+  const dim3 grid(sh.strips, sh.blocks);
+  const actg::Launch l{s, grid, n, cols / 8, sh.tx, sh.rows_per, db ? part : nullptr, st};
+  switch (act) {
+    case PRISM_ACT_RELU:
+      actg::run<PRISM_ACT_RELU>(l, Z8 != nullptr);
+      break;
+    case PRISM_ACT_SILU:
+      actg::run<PRISM_ACT_SILU>(l, Z8 != nullptr);
+      break;
+    case PRISM_ACT_GELU:
+      actg::run<PRISM_ACT_GELU>(l, Z8 != nullptr);
+      break;
+    default:
+      actg::act_grad_kernel<PRISM_ACT_NONE, false>
+          <<<grid, actg::kThreads, 0, st>>>(s, n, l.vecs, l.tx, l.rows_per, l.part);
+  }
+  count_launches(1);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !db) return e;
+  actg::bias_grad_kernel<<<(cols + 31) / 32, 256, 0, st>>>(part, sh.blocks, cols, db, db_fp32);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace prism

@@ -95,6 +95,23 @@ cudaError_t make_rows_map(CUtensorMap *map, const void *base, long long rows, in
 cudaError_t make_bf16_map(CUtensorMap *map, const void *base, int rank, const unsigned long long *dims,
                           const unsigned long long *strides, const unsigned *box);
 
+// 2-D tensor map: rows of `cols` elements `ld` elements apart, box box_cols x
+// box_rows; bf16 and fp32 with the 128-byte swizzle (box rows of 128 bytes),
+// bytes without one.
+enum MapType { MAP_BF16, MAP_F32, MAP_U8 };
+cudaError_t make_map_2d(CUtensorMap *map, MapType type, const void *base, long long cols, long long rows, long long ld,
+                        int box_cols, int box_rows);
+
+// act_grad.cu: dZ = dY act'(Z) (nothing to write without an activation) and
+// db = its column sums, through `part` (act_grad_part_bytes; db may be NULL)
+size_t act_grad_part_bytes(long long n, int cols);
+cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, long long ldy, const uint16_t *Z,
+                            long long ldz, const prism_ckpt8_t *Z8, uint16_t *dZ, float *part, void *db, int db_fp32,
+                            cudaStream_t st);
+
+// SMs of the current device (148 where there is none)
+int device_sm_count();
+
 // host-side count of kernel launches (prism_kernel_launches)
 void count_launches(int n);
 

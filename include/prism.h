@@ -13,6 +13,11 @@
  *   prism_attn_fwd  exact attention of every query over the tokens of its
  *                   selected key blocks; output in natural token order.
  *   prism_attn_bwd  gradients through the same selected blocks only.
+ * Around it, for the layer's other work on the video tokens:
+ *   prism_linear_fwd, prism_linear_bwd   a linear map with bias, activation
+ *                   and residual, and its gradients.
+ *   prism_ckpt8_pack, prism_ckpt8_unpack   activations held in 8 bits between
+ *                   the forward and the backward.
  *
  * Conventions shared by every call
  *   Layout.  Batch 1.  Natural raster token order n = (t*H + y)*W + x over
@@ -365,6 +370,116 @@ int prism_attn_bwd(const prism_params *p, const prism_plan_t *plan,
                    int grad_fp32, int deterministic, void *workspace,
                    size_t ws_bytes, prism_stream_t stream);
 
+/*
+ * An activation checkpoint in 8 bits: a matrix [n][width] held as signed 8-bit
+ * codes and, for every block of 32 channels of a row, one power-of-two scale.
+ *   codes   int8 [n][ld]; channels at index >= width hold 0.  16-byte aligned.
+ *   scales  uint8 [n][ld / 32]: scale byte s stands for 2^(s - 127).  4-byte
+ *           aligned.  Blocks that start at or beyond width are unspecified.
+ *   ld      width rounded up to a multiple of 128.
+ * The value of a channel is code * 2^(s - 127), exact in bf16.  s is the
+ * smallest integer >= 1 with max|x| <= 127 * 2^(s - 127) over the block, and
+ * the code is x / 2^(s - 127) rounded to nearest, ties to even: each value is
+ * off by at most half a scale, 2^-7 of the block's largest.  Values below 2^-127
+ * become 0.  A block that holds an infinity or NaN has s = 255 and codes 0 and
+ * stands for 32 NaNs; finite values above 127 * 2^121 are held as that value.
+ */
+typedef struct prism_ckpt8_t {
+  int8_t *codes;
+  uint8_t *scales;
+  int64_t ld;
+} prism_ckpt8_t;
+
+/*
+ * prism_ckpt8_pack -- the checkpoint of an activation, e.g. a tensor
+ * [N][heads][head_dim] taken as [N][heads * head_dim].
+ *   x         bf16 [n][ld] rows; the first `width` elements of each are read.
+ *             16-byte aligned.
+ *   n         rows, 0 <= n < 2^31; 0 launches nothing.
+ *   width     channels, a positive multiple of 8, at most 2^20.
+ *   ld        row stride of x in elements, a multiple of 8, >= width.
+ *   out       arrays to fill (host struct of device pointers).
+ * prism_ckpt8_unpack -- the activation back: x[n][ld] = code * scale; elements
+ * of x at index >= width of a row are left as they were.
+ * Return PRISM_OK, PRISM_ERR_INVALID_ARG or PRISM_ERR_CUDA.
+ */
+int prism_ckpt8_pack(const uint16_t *x, int64_t n, int32_t width, int64_t ld,
+                     const prism_ckpt8_t *out, prism_stream_t stream);
+int prism_ckpt8_unpack(const prism_ckpt8_t *in, int64_t n, int32_t width,
+                       uint16_t *x, int64_t ld, prism_stream_t stream);
+
+/*
+ * A linear map of n tokens from `in` to `out` channels with an activation.
+ *   n        tokens, 0 <= n < 2^30.
+ *   in, out  channels, positive multiples of 8, at most 65536.
+ *   act      PRISM_ACT_NONE, PRISM_ACT_RELU, PRISM_ACT_SILU, or
+ *            PRISM_ACT_GELU (tanh form:
+ *            z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))).
+ */
+enum { PRISM_ACT_NONE = 0, PRISM_ACT_RELU = 1, PRISM_ACT_SILU = 2, PRISM_ACT_GELU = 3 };
+typedef struct prism_linear_t {
+  int64_t n;
+  int32_t in, out;
+  int32_t act;
+} prism_linear_t;
+
+/* Bytes of workspace prism_linear_fwd (backward = 0) or prism_linear_bwd
+ * (backward = 1: any choice of gradients, bf16 or checkpointed inputs) needs on
+ * the current device (0 on an invalid description). */
+size_t prism_linear_workspace_size(const prism_linear_t *l, int backward);
+
+/*
+ * prism_linear_fwd -- Z = X W^T + bias, Y = act(Z) + R.
+ *   X      bf16 [n][ldx] (first `in` elements of each row).
+ *   W      bf16 [out][in], contiguous (the layout of a linear layer's weight).
+ *   bias   bf16 [out], or NULL.
+ *   R      bf16 [n][ldr], or NULL: the residual.  R may be Y itself (same
+ *          pointer and stride): the sum is then formed in place.
+ *   Y      bf16 [n][ldy].
+ *   Z      bf16 [n][out] contiguous, or NULL: the pre-activation, saved for the
+ *          backward.
+ *   Z8     the same as a checkpoint, or NULL: quantised from the fp32
+ *          pre-activation.  Not together with Z.
+ * ldx, ldr, ldy are row strides in elements, multiples of 8.  All pointers are
+ * 16-byte aligned.  Other than R = Y, outputs may overlap no input.
+ * Products are accumulated in fp32; bias, activation and residual are applied
+ * in fp32, and Y (and Z) rounded to bf16 once.
+ * Returns PRISM_OK, PRISM_ERR_INVALID_ARG, PRISM_ERR_CAPACITY or
+ * PRISM_ERR_CUDA; a kernel that gives up on an internal wait records
+ * PRISM_ERR_TIMEOUT in the workspace (prism_workspace_status).
+ */
+int prism_linear_fwd(const prism_linear_t *l, const uint16_t *X, int64_t ldx,
+                     const uint16_t *W, const uint16_t *bias, const uint16_t *R,
+                     int64_t ldr, uint16_t *Y, int64_t ldy, uint16_t *Z,
+                     const prism_ckpt8_t *Z8, void *workspace, size_t ws_bytes,
+                     prism_stream_t stream);
+
+/*
+ * prism_linear_bwd -- gradients of prism_linear_fwd:
+ *   dZ = dY * act'(Z),  dX = dZ W,  dW = dZ^T X,  db = column sums of dZ.
+ * (The gradient of R is dY.)
+ *   dY      bf16 [n][lddy].
+ *   X, X8   the forward's input: bf16 [n][ldx], or its checkpoint (the other
+ *           NULL).  Needed for dW.  The products read the checkpoint's codes;
+ *           X is not restored in memory.
+ *   W       bf16 [out][in].  Needed for dX.
+ *   Z, Z8   the forward's pre-activation, bf16 [n][ldz] or a checkpoint (the
+ *           other NULL).  Needed unless act is PRISM_ACT_NONE (then ignored).
+ *   dX      bf16 [n][in], or NULL.
+ *   dW, db  [out][in] and [out], or NULL: bf16 when grad_fp32 == 0, fp32 else.
+ * dZ is rounded to bf16 for the two products (the operand type of the tensor
+ * cores, and of dY itself); db sums the fp32 values.  Every sum is held in
+ * fp32 and taken in a fixed order: the outputs are bitwise reproducible.
+ * With n = 0, dW and db are zero.
+ * Returns as prism_linear_fwd.
+ */
+int prism_linear_bwd(const prism_linear_t *l, const uint16_t *dY, int64_t lddy,
+                     const uint16_t *X, int64_t ldx, const prism_ckpt8_t *X8,
+                     const uint16_t *W, const uint16_t *Z, int64_t ldz,
+                     const prism_ckpt8_t *Z8, uint16_t *dX, void *dW, void *db,
+                     int grad_fp32, void *workspace, size_t ws_bytes,
+                     prism_stream_t stream);
+
 /* Waits on `stream` and returns the status a kernel recorded in
  * `workspace`: PRISM_OK, PRISM_ERR_TIMEOUT, PRISM_ERR_RANGE (an attention
  * call met an infinite or NaN Q/K/V/dO value), PRISM_ERR_UNSUPPORTED (the
@@ -380,8 +495,9 @@ const char *prism_last_error(void);
  * (host-side counter, incremented at every launch; never reset). */
 uint64_t prism_kernel_launches(void);
 
-/* Optional timing of the library's kernels, for measurement (not meant to be
- * toggled by one thread while another launches through the library).  When
+/* Optional timing of the attention path's kernels, for measurement (not meant
+ * to be toggled by one thread while another launches through the library; the
+ * linear maps and the checkpoints, one to four launches a call, carry none).  When
  * enabled, every kernel launch of the path is bracketed by a CUDA event pair
  * recorded on its launching stream.
  * prism_kernel_timing(1) clears the records and enables; (0) clears and
