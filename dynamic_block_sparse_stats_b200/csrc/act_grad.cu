@@ -9,8 +9,7 @@
 // order.  Without an activation dZ is dY itself and only the sums are taken.
 #include <algorithm>
 
-#include "ckpt8.cuh"
-#include "internal.h"
+#include "gemm.cuh"
 
 namespace prism {
 namespace actg {
@@ -18,28 +17,34 @@ namespace actg {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
 
-// act'(z) in fp32, with p = 1 / (1 + e^-v).
-//   silu = z p(z):             slope p (1 + z (1 - p))
+// act'(z) of a pair in fp32, with p = 1 / (1 + e^-v).
+//   silu = z p(z):             slope p + z p (1 - p)
 //   gelu (tanh form) = z p(v), v = 2 sqrt(2/pi) (z + 0.044715 z^3): slope
 //                              p + z p (1 - p) v'
 // z is clamped where p is 0 or 1 to the last bit (e^-v overflows or vanishes), so
 // that no product of infinity and zero arises.  A NaN stays one (a restored
 // checkpoint block that held a non-finite value).
+__device__ __forceinline__ float clamp_nan(float x, float far) {
+  float y;
+  asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, t, %3;\n\t}" : "=f"(y) : "f"(x), "f"(far), "f"(-far));
+  return y;
+}
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (ACT == PRISM_ACT_RELU) return z > 0.f ? 1.f : (z != z ? z : 0.f);
+__device__ __forceinline__ float2 act_slope(float2 z) {
+  if constexpr (ACT == PRISM_ACT_RELU)
+    return make_float2(z.x > 0.f ? 1.f : (z.x != z.x ? z.x : 0.f), z.y > 0.f ? 1.f : (z.y != z.y ? z.y : 0.f));
   constexpr float kFar = ACT == PRISM_ACT_SILU ? 100.f : 30.f;
-  const float c = fminf(fmaxf(z, -kFar), kFar);
-  float s;
+  const float2 one = make_float2(1.f, 1.f);
+  const float2 c = make_float2(clamp_nan(z.x, kFar), clamp_nan(z.y, kFar));
   if constexpr (ACT == PRISM_ACT_SILU) {
-    const float p = __fdividef(1.f, 1.f + __expf(-c));
-    s = p * fmaf(c, 1.f - p, 1.f);
+    const float2 p = gemm::logistic2(fmul2(c, make_float2(-gemm::kLog2e, -gemm::kLog2e)));
+    return ffma2(fmul2(c, p), fsub2(one, p), p);
   } else {
-    const float z2 = c * c;
-    const float p = __fdividef(1.f, 1.f + __expf(-1.5957691216057308f * fmaf(0.044715f * z2, c, c)));
-    s = fmaf(c * p * (1.f - p), 1.5957691216057308f * fmaf(0.134145f, z2, 1.f), p);
+    constexpr float k = gemm::kGelu2;
+    const float2 z2 = fmul2(c, c);
+    const float2 p = gemm::logistic2(fmul2(c, ffma2(z2, -0.044715f * k * gemm::kLog2e, -k * gemm::kLog2e)));
+    return ffma2(fmul2(fmul2(c, p), fsub2(one, p)), ffma2(z2, 0.134145f * k, k), p);
   }
-  return z != z ? z : s;
 }
 
 struct Src {
@@ -62,7 +67,7 @@ __global__ void __launch_bounds__(kThreads)
   const int cv = blockIdx.x * tx + cx;
   const long long r0 = (long long)blockIdx.y * rows_per;
   const long long r1 = r0 + rows_per < n ? r0 + rows_per : n;
-  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float2 sum[4] = {};
   if (cv < vecs) {
     for (long long r = r0 + ry; r < r1; r += (long long)rows_step * kUnroll) {
       uint4 d[kUnroll], z[kUnroll];
@@ -100,26 +105,25 @@ __global__ void __launch_bounds__(kThreads)
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float lo = bf16lo(dw[k]) * act_slope<ACT>(bf16lo(zw[k]));
-            const float hi = bf16hi(dw[k]) * act_slope<ACT>(bf16hi(zw[k]));
-            sum[2 * k] += lo;
-            sum[2 * k + 1] += hi;
-            o[k] = pack_bf16(lo, hi);
+            const float2 g = fmul2(make_float2(bf16lo(dw[k]), bf16hi(dw[k])),
+                                   act_slope<ACT>(make_float2(bf16lo(zw[k]), bf16hi(zw[k]))));
+            sum[k] = fadd2(sum[k], g);
+            o[k] = pack_bf16(g.x, g.y);
           }
           s.dZ[rr * vecs + cv] = make_uint4(o[0], o[1], o[2], o[3]);
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            sum[2 * k] += bf16lo(dw[k]);
-            sum[2 * k + 1] += bf16hi(dw[k]);
-          }
+          for (int k = 0; k < 4; ++k) sum[k] = fadd2(sum[k], make_float2(bf16lo(dw[k]), bf16hi(dw[k])));
         }
       }
     }
   }
   if (!part) return;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) red[threadIdx.x][k] = sum[k];
+  for (int k = 0; k < 4; ++k) {
+    red[threadIdx.x][2 * k] = sum[k].x;
+    red[threadIdx.x][2 * k + 1] = sum[k].y;
+  }
   __syncthreads();
   // 8 * tx columns, summed over the row lanes
   for (int c = threadIdx.x; c < 8 * tx; c += kThreads) {

@@ -48,24 +48,25 @@ __device__ __forceinline__ uint32_t ckpt8_code4(float a, float b, float c, float
 }
 
 // one block held by one thread: returns s, codes in q
-__device__ __forceinline__ uint32_t ckpt8_quantise(const float (&v)[32], uint32_t (&q)[8]) {
+__device__ __forceinline__ uint32_t ckpt8_quantise(const float2 (&v)[16], uint32_t (&q)[8]) {
   // magnitudes as integers: a NaN compares above everything, so it is never lost
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  for (int i = 0; i < 16; ++i)
+    top = max(top, max(__float_as_uint(v[i].x) & 0x7fffffffu, __float_as_uint(v[i].y) & 0x7fffffffu));
   const uint32_t s = ckpt8_scale(top);
   const float inv = ckpt8_inverse(s);
   if (top <= kCkptTop) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = ckpt8_code4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], inv);
+    for (int i = 0; i < 8; ++i) q[i] = ckpt8_code4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y, inv);
   } else if (s == kCkptBad) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = 0;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      q[i] = ckpt8_code4(ckpt8_clamp(v[4 * i]), ckpt8_clamp(v[4 * i + 1]), ckpt8_clamp(v[4 * i + 2]),
-                         ckpt8_clamp(v[4 * i + 3]), inv);
+      q[i] = ckpt8_code4(ckpt8_clamp(v[2 * i].x), ckpt8_clamp(v[2 * i].y), ckpt8_clamp(v[2 * i + 1].x),
+                         ckpt8_clamp(v[2 * i + 1].y), inv);
   }
   return s;
 }

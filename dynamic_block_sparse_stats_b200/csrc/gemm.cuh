@@ -13,7 +13,7 @@
 // swizzled rows: K-major [rows][64 k], MN-major [64 k][64 mn] per 64 columns.
 //
 // B8: operand B (MN-major) is an 8-bit checkpoint (ckpt8.cu).  TMA brings the
-// codes, four warps turn them into bf16 (exact: 8-bit integer times a power of
+// codes, two teams of warps turn them into bf16 (exact: 8-bit integer times a power of
 // two) in the swizzled layout the tensor cores read.
 //
 // SUM: the tensor cores add into their fp32 accumulator with truncation, an
@@ -24,8 +24,8 @@
 // chain runs in the other accumulator.
 //
 // Roles (warps): 0 TMA producer, 1 MMA issuer (CTA 0 of a pair), 2 TMEM owner,
-// 3 idle, 4-11 epilogue (two accumulators in TMEM alternate, so the epilogue of
-// one tile runs under the products of the next), 12-15 the converters of B8.
+// 3 producer of the codes (B8), 4-11 epilogue (two accumulators in TMEM alternate, so the epilogue of
+// one tile runs under the products of the next), from 12 the converters of B8.
 #pragma once
 
 #include "ckpt8.cuh"
@@ -38,7 +38,8 @@ namespace gemm {
 constexpr int BK = 64;  // contraction per stage: one 128-byte swizzle row of bf16
 constexpr int kEpiWarps = 8;
 constexpr int kStageBuf = 4096;  // one epilogue staging buffer: 32 rows x 128 bytes
-constexpr int kConvWarps = 4;
+constexpr int kConvTeams = 2;  // teams of converter warps, taking the stages in turn
+constexpr int kConvTeam = 4;   // warps of a team
 constexpr int kChain = 8;  // stages per accumulator chain when SUM
 
 template <int CG_, int BN_, bool A_MN_, bool B_MN_, bool B8_ = false, bool SUM_ = false>
@@ -50,22 +51,32 @@ struct Cfg {
   static constexpr int A_BYTES = 128 * BK * 2;
   static constexpr int B_BYTES = BNC * BK * 2;
   static constexpr int Q_BYTES = B8 ? BNC * BK : 0;  // codes of the stage's B
-  static constexpr int STAGE = A_BYTES + B_BYTES + Q_BYTES;
-  static constexpr int EPI = kEpiWarps * 2 * kStageBuf;
+  // rings of operand stages: A with B; with B8 three of their own, so that the
+  // codes arrive and are converted well ahead of the products
+  static constexpr int STAGE = B8 ? A_BYTES : A_BYTES + B_BYTES;
+  static constexpr int NBUF = B8 ? 1 : 2;  // staging buffers of an epilogue warp
+  static constexpr int EPI = kEpiWarps * NBUF * kStageBuf;
   static constexpr int NST_FIT = (232448 - 2048 - EPI) / STAGE;
-  static constexpr int NST = NST_FIT < 6 ? NST_FIT : 6;
-  static constexpr int OFF_EPI = NST * STAGE;
+  static constexpr int NST = B8 ? 5 : NST_FIT < 6 ? NST_FIT : 6;
+  static constexpr int NB = B8 ? 4 : NST;
+  static constexpr int NQ = 5;
+  static constexpr int OFF_B = B8 ? NST * STAGE : A_BYTES;
+  static constexpr int B_PITCH = B8 ? B_BYTES : STAGE;
+  static constexpr int OFF_Q = NST * STAGE + NB * B_BYTES;
+  static constexpr int OFF_EPI = B8 ? OFF_Q + NQ * Q_BYTES : NST * STAGE;
   static constexpr int OFF_BAR = OFF_EPI + EPI;
-  static constexpr int SMEM = OFF_BAR + 1024 + 1024;  // barriers; slack to align the base to 1024
-  static constexpr int THREADS = B8 ? 512 : 384;
+  static constexpr int OFF_SC = OFF_BAR + 1024;        // B8: scale words of the codes' stages, one per token
+  static constexpr int SMEM = OFF_SC + (B8 ? NQ * BK * 4 : 0) + 1024;  // slack to align the base to 1024
+  static constexpr int THREADS = B8 ? 384 + 32 * kConvTeams * kConvTeam : 384;
+  static_assert(SMEM <= 232448, "shared memory");
   static constexpr int TMEM_COLS = 2 * BN;
-  static constexpr bool REGS = B8 && SUM && BN == 256;  // registers move between warpgroups
   static_assert(!B8 || (B_MN && BNC == 128), "the checkpoint operand comes in 128-channel columns");
 };
 
 struct Bars {
   uint64_t full[6], empty[6];          // operand stages: filled (CTA 0's), consumed (each CTA's own)
-  uint64_t qfull[6];                   // B8: codes arrived (each CTA's own)
+  uint64_t bfull[6], bempty[6];        // B8: B converted (CTA 0's), consumed (each CTA's own)
+  uint64_t qfull[6], qempty[6];        // B8: codes arrived, converted (each CTA's own)
   uint64_t acc_full[2], acc_empty[2];  // accumulators: complete (each CTA's own), read (CTA 0's)
   uint64_t res[kEpiWarps][2];          // residual tiles of each epilogue warp
   uint64_t drain;                      // single use, after an abort
@@ -166,36 +177,17 @@ __device__ __forceinline__ uint32_t map_to_cta0(const void *p) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
   return r;
 }
+// Arrive on CTA 0's barrier.  What it publishes is not read through the generic
+// proxy by CTA 0: accumulators have been read (tcgen05.wait::ld), or this CTA's
+// own shared memory has been written and fenced for the tensor cores that read it
+// here.  So the arrival carries no cluster-scope release, which would wait for
+// every outstanding memory operation (measured: 1.5 us a stage in the converters).
 template <int CG>
 __device__ __forceinline__ void arrive_cta0(uint64_t *bar) {
   if constexpr (CG == 1) {
     mbar_arrive(bar);
   } else {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to_cta0(bar)) : "memory");
-  }
-}
-template <int CG>
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, int *status, int where) {
-  if constexpr (CG == 1) {
-    return mbar_wait(bar, parity, status, where);
-  } else {
-    long long t0 = 0;
-    for (int spin = 0;; ++spin) {
-      uint32_t ok;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity)
-          : "memory");
-      if (ok) return true;
-      if (spin == 0) {
-        t0 = clock64();
-      } else if (clock64() - t0 > kWaitLimitCycles) {
-        record_timeout(status, where);
-        return false;
-      }
-    }
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_cta0(bar)) : "memory");
   }
 }
 // TMA load into this CTA's shared memory, counted on CTA 0's barrier
@@ -265,13 +257,20 @@ __device__ __forceinline__ void tmem_dealloc_g(uint32_t t, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(ncols) : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
+// four bytes global -> shared without a register in between (zeros unless `in`)
+__device__ __forceinline__ void copy4_async(void *dst, const void *src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0) : "memory");
+}
+// arrive on `bar` once this thread's copies so far have landed
+__device__ __forceinline__ void copy_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -282,15 +281,28 @@ __device__ __forceinline__ void setmaxnreg_dec() {
 }
 
 // ---------------------------------------------------------------------------
-// activations (fp32).  gelu is the tanh form: z * sigmoid(2u),
-// u = sqrt(2/pi) (z + 0.044715 z^3).
+// activations of a pair (fp32).  gelu is the tanh form, z / (1 + e^-v) with
+// v = 2 sqrt(2/pi) (z + 0.044715 z^3); silu is the same with v = z.
 // ---------------------------------------------------------------------------
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGelu2 = 1.5957691216057308f;  // 2 sqrt(2/pi)
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// 1 / (1 + 2^w)
+__device__ __forceinline__ float2 logistic2(float2 w) {
+  const float2 d = fadd2(make_float2(ex2f(w.x), ex2f(w.y)), make_float2(1.f, 1.f));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
 template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (ACT == PRISM_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
-  if constexpr (ACT == PRISM_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
-  if constexpr (ACT == PRISM_ACT_GELU) return __fdividef(z, 1.f + __expf(-kGelu2 * fmaf(0.044715f * z * z, z, z)));
+__device__ __forceinline__ float2 act_value(float2 z) {
+  if constexpr (ACT == PRISM_ACT_RELU)
+    return make_float2(z.x > 0.f ? z.x : (z.x != z.x ? z.x : 0.f), z.y > 0.f ? z.y : (z.y != z.y ? z.y : 0.f));
+  if constexpr (ACT == PRISM_ACT_SILU) return fmul2(z, logistic2(fmul2(z, make_float2(-kLog2e, -kLog2e))));
+  if constexpr (ACT == PRISM_ACT_GELU)
+    return fmul2(z, logistic2(fmul2(z, ffma2(fmul2(z, z), -0.044715f * kGelu2 * kLog2e, -kGelu2 * kLog2e))));
   return z;
 }
 
@@ -298,9 +310,15 @@ __device__ __forceinline__ float act_value(float z) {
 // epilogues
 // ---------------------------------------------------------------------------
 template <int ACT>
-__device__ __forceinline__ void act32(float (&v)[32]) {
+__device__ __forceinline__ void act32(float2 (&v)[16]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = act_value<ACT>(v[i]);
+  for (int i = 0; i < 16; ++i) v[i] = act_value<ACT>(v[i]);
+}
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) { return make_float2(bf16lo(w), bf16hi(w)); }
+// eight values of v from index i, rounded
+__device__ __forceinline__ uint4 pack8(const float2 (&v)[16], int i) {
+  return make_uint4(pack_bf16(v[i].x, v[i].y), pack_bf16(v[i + 1].x, v[i + 1].y), pack_bf16(v[i + 2].x, v[i + 2].y),
+                    pack_bf16(v[i + 3].x, v[i + 3].y));
 }
 
 // one warp's 32 x 32 fp32 values (thread = row) through a staging buffer to
@@ -339,7 +357,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
   constexpr int PER = NCH > 1 ? NCH / 2 : 1;  // chunks of this warp
   const int c_lo = NCH > 1 ? half * PER : 0;
   const int n_ch = NCH > 1 ? PER : (half == 0 ? 1 : 0);
-  uint8_t *buf = staging + ew * 2 * kStageBuf;
+  uint8_t *buf = staging + ew * C::NBUF * kStageBuf;
   const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
   const int sw = lane & 7;
   const bool z16 = args.save_z == 1;
@@ -381,9 +399,9 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
           uint32_t v[32];
           tmem_ld32(acc + g * 32, v);
           tmem_wait_ld();
-          if (lane == 0) store_wait_read<1>();
+          if (lane == 0) store_wait_read<C::NBUF - 1>();
           __syncwarp();
-          stage_fp32(&mapZ, buf + (g & 1) * kStageBuf, v, lane, c_lo * 64 + g * 32,
+          stage_fp32(&mapZ, buf + (g & (C::NBUF - 1)) * kStageBuf, v, lane, c_lo * 64 + g * 32,
                      sg.slot * C::BM + rank * 128 + q4 * 32, true);
         }
       }
@@ -391,7 +409,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
       for (int c = 0; c < (parts ? 0 : n_ch); ++c) {
         const int col0 = n0 + c * 64;
         const bool in = rows_in && col0 < args.cols;
-        const int yb = z16 ? 0 : c;
+        const int yb = z16 || C::NBUF == 1 ? 0 : c;
         if (z16 && c > 0) {
           if (lane == 0) store_wait_read<0>();
           __syncwarp();
@@ -401,7 +419,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
         if (!args.has_res) {
           // this buffer's last store was the one before the last (z16: the last)
           if (lane == 0) {
-            if (z16 || C::BN < 256)
+            if (z16 || C::BN < 256 || C::NBUF == 1)
               store_wait_read<0>();
             else
               store_wait_read<1>();
@@ -416,9 +434,9 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
           uint32_t u[32];
           tmem_ld32(acc + c * 64 + g * 32, u);
           tmem_wait_ld();
-          float v[32];
+          float2 v[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+          for (int i = 0; i < 16; ++i) v[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
           if (args.bias) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -426,19 +444,14 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
                 const uint4 b = __ldg(reinterpret_cast<const uint4 *>(args.bias + cg0) + i);
                 const uint32_t w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  v[8 * i + 2 * k] += bf16lo(w[k]);
-                  v[8 * i + 2 * k + 1] += bf16hi(w[k]);
-                }
+                for (int k = 0; k < 4; ++k) v[4 * i + k] = fadd2(v[4 * i + k], bf16_pair(w[k]));
               }
             }
           }
           if (z16) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4 *>(row + kStageBuf + (((g * 4 + i) ^ sw) << 4)) =
-                  make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                             pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+              *reinterpret_cast<uint4 *>(row + kStageBuf + (((g * 4 + i) ^ sw) << 4)) = pack8(v, 4 * i);
           } else if (args.save_z == 2) {
             uint32_t q[8];
             const uint32_t sc = ckpt8_quantise(v, q);
@@ -475,13 +488,9 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
               const uint4 r = *p;
               const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                v[8 * i + 2 * k] += bf16lo(w[k]);
-                v[8 * i + 2 * k + 1] += bf16hi(w[k]);
-              }
+              for (int k = 0; k < 4; ++k) v[4 * i + k] = fadd2(v[4 * i + k], bf16_pair(w[k]));
             }
-            *p = make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                            pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+            *p = pack8(v, 4 * i);
           }
         }
         if (!ok) break;
@@ -520,7 +529,7 @@ __device__ __forceinline__ void epilogue_sum(const CUtensorMap &mapY, const CUte
   const Sched &s = args.s;
   const int ew = warp - 4, q4 = warp & 3, half = ew >> 2;
   constexpr int COLS = C::BN / 2;
-  uint8_t *buf = staging + ew * 2 * kStageBuf;
+  uint8_t *buf = staging + ew * C::NBUF * kStageBuf;
   const uint32_t acc0 = tmem + half * COLS + ((uint32_t)(q4 * 32) << 16);
   SegIter it(s, group);
   Seg sg;
@@ -536,12 +545,12 @@ __device__ __forceinline__ void epilogue_sum(const CUtensorMap &mapY, const CUte
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int g = 0; g < COLS / 16; ++g) {
-        uint32_t v[16];
-        tmem_ld16(acc0 + ab * C::BN + g * 16, v);
+      for (int g = 0; g < COLS / 8; ++g) {
+        uint32_t v[8];
+        tmem_ld8(acc0 + ab * C::BN + g * 8, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum[g * 16 + i] += __uint_as_float(v[i]);
+        for (int i = 0; i < 8; ++i) sum[g * 8 + i] += __uint_as_float(v[i]);
       }
       tc_fence_before();
       __syncwarp();
@@ -552,16 +561,16 @@ __device__ __forceinline__ void epilogue_sum(const CUtensorMap &mapY, const CUte
     const int n0 = (sg.tile % s.tiles_n) * C::BN + half * COLS;
 #pragma unroll
     for (int g = 0; g < COLS / 32; ++g) {
-      if (lane == 0) store_wait_read<1>();
+      if (lane == 0) store_wait_read<C::NBUF - 1>();
       __syncwarp();
       uint32_t v[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[g * 32 + i]);
       if (sg.slot >= 0)
-        stage_fp32(&mapZ, buf + (g & 1) * kStageBuf, v, lane, half * COLS + g * 32,
+        stage_fp32(&mapZ, buf + (g & (C::NBUF - 1)) * kStageBuf, v, lane, half * COLS + g * 32,
                    sg.slot * C::BM + rank * 128 + q4 * 32, true);
       else
-        stage_fp32(&mapY, buf + (g & 1) * kStageBuf, v, lane, n0 + g * 32, m0,
+        stage_fp32(&mapY, buf + (g & (C::NBUF - 1)) * kStageBuf, v, lane, n0 + g * 32, m0,
                    m0 < args.rows && n0 + g * 32 < args.cols);
     }
   }
@@ -588,10 +597,13 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
   int *status = args.status;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(&bar.full[i], 1 + (C::B8 ? kConvWarps * CG : 0));
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
-      mbar_init(&bar.qfull[i], 1);
+      mbar_init(&bar.bfull[i], kConvTeam * CG);
+      mbar_init(&bar.bempty[i], 1);
+      mbar_init(&bar.qfull[i], 1 + 32);  // the codes' TMA, and warp 3's scale copies
+      mbar_init(&bar.qempty[i], kConvTeam);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.acc_full[i], 1);
@@ -610,11 +622,12 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = bar.tmem_base;
   const auto aborted = [&] { return *reinterpret_cast<volatile int *>(&bar.abort) != 0; };
-  // 512 threads and 128 sums in each of the epilogue's: the launch gives each of
-  // the four warpgroups 128 registers a thread; 64 + 176 + 176 + 96 is the same total.
-  if constexpr (C::REGS) {
+  // B8: the launch gives each of the five warpgroups 96 registers a thread.  The
+  // epilogue needs more (SUM: 128 sums), the others less; the totals are the same:
+  // 64 + 2 * 144 + 2 * 64 = 480, 64 + 2 * 128 + 2 * 80 = 480.
+  if constexpr (C::B8) {
     if (warp < 4) setmaxnreg_dec<64>();
-    if (warp >= 12) setmaxnreg_dec<96>();
+    if (warp >= 12) setmaxnreg_dec<C::SUM ? 64 : 80>();
   }
 
   if (warp == 0) {
@@ -631,12 +644,12 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
         const int n0 = (sg.tile % s.tiles_n) * C::BN + (int)rank * C::BNC;
         for (int k = sg.k0; k < sg.k1; ++k, ++j) {
           const int st = j % NST;
-          if (j >= NST && !(ok = wait_cluster<CG>(&bar.empty[st], ((j / NST) - 1) & 1, status, 401))) break;
+          if (j >= NST && !(ok = mbar_wait(&bar.empty[st], ((j / NST) - 1) & 1, status, 401))) break;
           if (aborted()) {
             ok = false;
             break;
           }
-          uint8_t *a = smem + st * C::STAGE, *b = a + C::A_BYTES;
+          uint8_t *a = smem + st * C::STAGE, *b = smem + C::OFF_B + st * C::B_PITCH;
           if (rank == 0) mbar_arrive_expect_tx(&bar.full[st], CG * (C::A_BYTES + (C::B8 ? 0 : C::B_BYTES)));
           if constexpr (C::A_MN) {
             load_2d<CG>(a, &mapA, &bar.full[st], m0, k * BK);
@@ -645,8 +658,7 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
             load_2d<CG>(a, &mapA, &bar.full[st], k * BK, m0);
           }
           if constexpr (C::B8) {
-            mbar_arrive_expect_tx(&bar.qfull[st], C::Q_BYTES);
-            tma_load_2d(b + C::B_BYTES, &mapB, &bar.qfull[st], n0, k * BK);
+            // warp 3 brings the codes
           } else if constexpr (C::B_MN) {
 #pragma unroll
             for (int c = 0; c < C::BNC; c += 64)
@@ -660,13 +672,12 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
         // every stage consumed: no copy is in flight, and the arrivals of the
         // last products on this CTA's barriers have landed
         for (int i = j > NST ? j - NST : 0; i < j; ++i)
-          wait_cluster<CG>(&bar.empty[i % NST], (i / NST) & 1, status, 402);
+          mbar_wait(&bar.empty[i % NST], (i / NST) & 1, status, 402);
       } else {
         // no copy may still be writing when the CTA leaves: CTA 0's barriers
         // count both CTAs' operand loads, and the pair leaves together
         bar.abort = 1;
         if (rank == 0) drain_loads(bar.full, NST, j, status, 403);
-        if constexpr (C::B8) drain_loads(bar.qfull, NST, j, status, 403);
       }
     }
   } else if (warp == 1) {
@@ -681,13 +692,18 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
         for (int k0 = sg.k0; ok && k0 < sg.k1; ++t) {
           const int k1 = C::SUM ? min(k0 + kChain, sg.k1) : sg.k1;
           const int ab = t & 1;
-          if (t >= 2 && !(ok = wait_cluster<CG>(&bar.acc_empty[ab], ((t >> 1) - 1) & 1, status, 404))) break;
+          if (t >= 2 && !(ok = mbar_wait(&bar.acc_empty[ab], ((t >> 1) - 1) & 1, status, 404))) break;
           tc_fence_after();
           for (int k = k0; k < k1; ++k, ++j) {
             const int st = j % NST;
-            if (!(ok = wait_cluster<CG>(&bar.full[st], (j / NST) & 1, status, 405))) break;
+            if (!(ok = mbar_wait(&bar.full[st], (j / NST) & 1, status, 405))) break;
             tc_fence_after();
-            const uint32_t a = smem_u32(smem + st * C::STAGE), b = a + C::A_BYTES;
+            const int sb = j % C::NB;
+            if constexpr (C::B8) {
+              if (!(ok = mbar_wait(&bar.bfull[sb], (j / C::NB) & 1, status, 412))) break;
+              tc_fence_after();
+            }
+            const uint32_t a = smem_u32(smem + st * C::STAGE), b = smem_u32(smem + C::OFF_B + sb * C::B_PITCH);
             // MN-major: 64-column chunks BK * 128 bytes apart, 8-k groups of 1024 bytes
             const uint64_t da = C::A_MN ? sdesc_sw128(a, BK * 128, 1024) : sdesc_sw128(a, 16, 1024);
             const uint64_t db = C::B_MN ? sdesc_sw128(b, BK * 128, 1024) : sdesc_sw128(b, 16, 1024);
@@ -696,6 +712,7 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
               mma<CG>(tmem + ab * C::BN, da + (C::A_MN ? (uint64_t)kk * 128 : kslice16(kk, 0)),
                       db + (C::B_MN ? (uint64_t)kk * 128 : kslice16(kk, 0)), idesc, (k > k0 || kk > 0) ? 1u : 0u);
             commit<CG>(&bar.empty[st]);
+            if constexpr (C::B8) commit<CG>(&bar.bempty[sb]);
           }
           if (ok) commit<CG>(&bar.acc_full[ab]);
           k0 = k1;
@@ -712,9 +729,45 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
       }
     }
     __syncwarp();
+  } else if (C::B8 && warp == 3) {
+    // ---------------------------------------------------------------- producer of the codes and scales
+    if constexpr (C::B8) {
+      if (lane == 0) prefetch_tensormap(&mapB);
+      const long long lds = args.b_ld / 32;
+      SegIter it(s, group);
+      Seg sg;
+      int j = 0;
+      bool ok = true;
+      while (ok && it.next(s, sg)) {
+        const int n0 = (sg.tile % s.tiles_n) * C::BN + (int)rank * C::BNC;
+        const bool cols_in = n0 < args.b_ld;
+        for (int k = sg.k0; k < sg.k1; ++k, ++j) {
+          const int sq = j % C::NQ;
+          if (j >= C::NQ) ok = mbar_wait(&bar.qempty[sq], ((j / C::NQ) - 1) & 1, status, 413);
+          if (!(ok = __all_sync(0xffffffffu, ok && !aborted()))) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bar.qfull[sq], C::Q_BYTES);
+            tma_load_2d(smem + C::OFF_Q + sq * C::Q_BYTES, &mapB, &bar.qfull[sq], n0, k * BK);
+          }
+          // a token's four scales of these 128 channels are one word
+#pragma unroll
+          for (int p = 0; p < BK; p += 32) {
+            const int tok = k * BK + p + lane;
+            const bool in = cols_in && tok < args.k_total;
+            copy4_async(smem + C::OFF_SC + (sq * BK + p + lane) * 4,
+                        in ? args.b_scales + (long long)tok * lds + (n0 >> 5) : args.b_scales, in);
+          }
+          copy_async_arrive(&bar.qfull[sq]);
+        }
+      }
+      if (!ok) bar.abort = 1;
+      copy_async_wait();
+      if (lane == 0) drain_loads(bar.qfull, C::NQ, j, status, 414);
+    }
+    __syncwarp();
   } else if (warp >= 4 && warp < 4 + kEpiWarps) {
     // ---------------------------------------------------------------- epilogue
-    if constexpr (C::REGS) setmaxnreg_inc<176>();
+    if constexpr (C::B8) setmaxnreg_inc<C::SUM ? 144 : 128>();
     if constexpr (C::SUM)
       epilogue_sum<C>(mapY, mapZ, args, bar, smem + C::OFF_EPI, tmem, group, (int)rank, warp, lane);
     else
@@ -722,73 +775,48 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
   } else if (C::B8 && warp >= 12) {
     // ---------------------------------------------------------------- converters of the checkpoint operand
     if constexpr (C::B8) {
-      const int cw = warp - 12;
-      // lane -> 16 channels (lane % 8) of token row cw * 16 + pass * 4 + lane / 8
+      // lane -> 16 channels (lane % 8) of token rows cw * ROWS + pass * 4 + lane / 8
+      constexpr int ROWS = BK / kConvTeam, PASS = ROWS / 4;
+      const int cw = (warp - 12) % kConvTeam, team = (warp - 12) / kConvTeam;
       const int unit = lane & 7, sub = lane >> 3;
-      const long long lds = args.b_ld / 32;
-      SegIter it(s, group), ahead(s, group);
-      Seg sg, ag;
-      // scales travel kAhead stages before their codes are due
-      constexpr int kAhead = 3;
-      uint32_t sc[kAhead][4];
-      bool more = ahead.next(s, ag);
-      int ak = more ? ag.k0 : 0;
-      const auto fetch = [&](uint32_t (&d)[4]) {
-        if (!more) return;
-        const int blk = (((ag.tile % s.tiles_n) * C::BN + (int)rank * C::BNC) >> 5) + (unit >> 1);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const int tok = ak * BK + cw * 16 + p * 4 + sub;
-          d[p] = (tok < args.k_total && blk < lds) ? __ldg(args.b_scales + (long long)tok * lds + blk) : 127u;
-        }
-        if (++ak == ag.k1) {
-          more = ahead.next(s, ag);
-          ak = more ? ag.k0 : 0;
-        }
-      };
-#pragma unroll
-      for (int a = 0; a < kAhead; ++a) fetch(sc[a]);
-      int j = 0, slot = 0;
+      const int r0 = cw * ROWS + sub;
+      SegIter it(s, group);
+      Seg sg;
+      int j = 0;
       bool ok = true;
-      // one stage: codes -> bf16 in the B buffer
-      const auto convert = [&](uint32_t (&scale)[4]) {
-        const int st = j % NST;
-        // the stage's codes are loaded only once its products are done, so
-        // their arrival also says that B's buffer may be written
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar.qfull[st], (j / NST) & 1, status, 410));
-        if (!ok) return;
-        uint8_t *b = smem + st * C::STAGE + C::A_BYTES;
-        const uint8_t *qs = b + C::B_BYTES;
-        uint4 q[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) q[p] = *reinterpret_cast<const uint4 *>(qs + (cw * 16 + p * 4 + sub) * 128 + unit * 16);
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const int r = cw * 16 + p * 4 + sub;
-          uint4 lo, hi;
-          ckpt8_restore16(q[p], scale[p], lo, hi);
-          uint8_t *row = b + (unit >> 2) * (BK * 128) + r * 128;
-          const int c0 = (unit & 3) * 2;
-          // the two 64-channel halves store their units in opposite order: no bank is hit twice
-          const int first = unit >> 2;
-          *reinterpret_cast<uint4 *>(row + (((c0 + first) ^ (r & 7)) << 4)) = first ? hi : lo;
-          *reinterpret_cast<uint4 *>(row + (((c0 + 1 - first) ^ (r & 7)) << 4)) = first ? lo : hi;
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_cta0<CG>(&bar.full[st]);
-        fetch(scale);
-        ++j;
-      };
       while (ok && it.next(s, sg)) {
-        for (int k = sg.k0; ok && k < sg.k1; ++k) {
-          if (slot == 0)
-            convert(sc[0]);
-          else if (slot == 1)
-            convert(sc[1]);
-          else
-            convert(sc[2]);
-          slot = slot == kAhead - 1 ? 0 : slot + 1;
+        for (int k = sg.k0; k < sg.k1; ++k, ++j) {
+          if (j % kConvTeams != team) continue;
+          const int sq = j % C::NQ, sb = j % C::NB;
+          ok = mbar_wait(&bar.qfull[sq], (j / C::NQ) & 1, status, 410);
+          const uint8_t *qs = smem + C::OFF_Q + sq * C::Q_BYTES + r0 * 128 + unit * 16;
+          const uint8_t *ss = smem + C::OFF_SC + (sq * BK + r0) * 4 + (unit >> 1);
+          uint4 q[PASS];
+          uint32_t sc[PASS];
+#pragma unroll
+          for (int p = 0; p < PASS; ++p) {
+            q[p] = *reinterpret_cast<const uint4 *>(qs + p * 512);
+            sc[p] = ss[p * 16];
+          }
+          if (j >= C::NB) ok = mbar_wait(&bar.bempty[sb], ((j / C::NB) - 1) & 1, status, 415) && ok;
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          // the two 64-channel halves store their units in opposite order: no bank is hit twice
+          const int first = unit >> 2, c0 = (unit & 3) * 2;
+          uint8_t *b = smem + C::OFF_B + sb * C::B_PITCH + first * (BK * 128) + r0 * 128;
+#pragma unroll
+          for (int p = 0; p < PASS; ++p) {
+            uint4 lo, hi;
+            ckpt8_restore16(q[p], sc[p], lo, hi);
+            const int x = (r0 + 4 * p) & 7;
+            *reinterpret_cast<uint4 *>(b + p * 512 + (((c0 + first) ^ x) << 4)) = first ? hi : lo;
+            *reinterpret_cast<uint4 *>(b + p * 512 + (((c0 + 1 - first) ^ x) << 4)) = first ? lo : hi;
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            arrive_cta0<CG>(&bar.bfull[sb]);
+            mbar_arrive(&bar.qempty[sq]);
+          }
         }
       }
       if (!ok) bar.abort = 1;
