@@ -7,6 +7,7 @@ A2V norm map fp32 [N].
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 from dataclasses import dataclass
@@ -414,6 +415,25 @@ def workspace_status(ws: torch.Tensor, stream=None) -> int:
         return _lib.load().prism_workspace_status(_ptr(ws), _stream(stream, dev))
 
 
+# ----------------------------------------------------------------------------- linear maps and checkpoints
+# These calls can be a few microseconds of GPU work, so what surrounds them is
+# kept short: no device switch where the tensors' device is current already, the
+# current stream by its raw handle, addresses as plain integers.
+_HERE = contextlib.nullcontext()
+
+
+def _on(dev):
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _handle(stream, dev) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 # ----------------------------------------------------------------------------- 8-bit activation checkpoints
 @dataclass
 class Ckpt8:
@@ -452,16 +472,19 @@ def _check_rows(t, name, shape=None):
         raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+    got = t.shape
+    if len(got) != 2 or (shape is not None and got != shape):
         want = "two dimensions" if shape is None else f"shape {tuple(shape)}"
-        raise ValueError(f"{name} must have {want}, got {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have {want}, got {tuple(got)}")
+    rows, cols = got
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} rows must be contiguous")
-    if t.shape[0] <= 1:
-        return t.shape[1]
-    if t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name} rows overlap (stride {t.stride(0)}, {t.shape[1]} channels)")
-    return t.stride(0)
+    if rows <= 1:
+        return cols
+    if ld < cols:
+        raise ValueError(f"{name} rows overlap (stride {ld}, {cols} channels)")
+    return ld
 
 
 def ckpt8_pack(x: torch.Tensor, out: Ckpt8 | None = None, stream=None) -> Ckpt8:
@@ -471,10 +494,10 @@ def ckpt8_pack(x: torch.Tensor, out: Ckpt8 | None = None, stream=None) -> Ckpt8:
     n, width = x.shape
     named = [("x", x)] + (_check_ckpt8(out, "out", n, width) if out is not None else [])
     dev = _check_devices(named)
-    with torch.cuda.device(dev):
+    with _on(dev):
         out = out if out is not None else alloc_ckpt8(n, width, dev)
         cs = out.c_struct()
-        check(_lib.load().prism_ckpt8_pack(_ptr(x), n, width, ld, C.byref(cs), _stream(stream, dev)))
+        check(_lib.load().prism_ckpt8_pack(_addr(x), n, width, ld, C.byref(cs), _handle(stream, dev)))
     return out
 
 
@@ -490,10 +513,10 @@ def ckpt8_unpack(c: Ckpt8, out: torch.Tensor | None = None, stream=None) -> torc
         ld = _check_rows(out, "out", (n, c.width))
         named.append(("out", out))
     dev = _check_devices(named)
-    with torch.cuda.device(dev):
+    with _on(dev):
         out = out if out is not None else torch.empty((n, c.width), dtype=torch.bfloat16, device=dev)
         cs = c.c_struct()
-        check(_lib.load().prism_ckpt8_unpack(C.byref(cs), n, c.width, _ptr(out), ld, _stream(stream, dev)))
+        check(_lib.load().prism_ckpt8_unpack(C.byref(cs), n, c.width, _addr(out), ld, _handle(stream, dev)))
     return out
 
 
@@ -521,9 +544,12 @@ class LinearGrads:
     ws: torch.Tensor
 
 
-def linear_workspace_size(n: int, cin: int, cout: int, act: int = ACT_NONE, backward: bool = False) -> int:
-    """Bytes of the `ws` buffer linear_fwd / linear_bwd takes for n tokens."""
-    size = _lib.load().prism_linear_workspace_size(C.byref(PrismLinear(n, cin, cout, act)), int(backward))
+def linear_workspace_size(n: int, cin: int, cout: int, act: int = ACT_NONE, backward: bool = False,
+                          x8: bool = False) -> int:
+    """Bytes of the `ws` buffer linear_fwd / linear_bwd takes for n tokens (x8:
+    linear_bwd with X as a Ckpt8)."""
+    mode = (2 if x8 else 1) if backward else 0
+    size = _lib.load().prism_linear_workspace_size(C.byref(PrismLinear(n, cin, cout, act)), mode)
     if size == 0:
         raise _lib.PrismError(_lib.PRISM_ERR_INVALID_ARG, _lib.load().prism_last_error().decode(errors="replace"))
     return size
@@ -561,7 +587,7 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
         _check_workspace(ws, "ws")
     dev = _check_devices(named)
     lib = _lib.load()
-    with torch.cuda.device(dev):
+    with _on(dev):
         Y = Y if Y is not None else torch.empty((n, cout), dtype=torch.bfloat16, device=dev)
         if Z is None and save is not None:
             Z = torch.empty_like(Y, memory_format=torch.contiguous_format) if save == "bf16" else \
@@ -569,9 +595,9 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
         l = PrismLinear(n, cin, cout, act)
         ws = ws if ws is not None else _workspace(lib.prism_linear_workspace_size(C.byref(l), 0), dev)
         z8 = Z.c_struct() if save == "ckpt8" else None
-        check(lib.prism_linear_fwd(C.byref(l), _ptr(X), ldx, _ptr(W), _ptr(bias), _ptr(residual), ldr, _ptr(Y), ldy,
-                                   _ptr(Z) if save == "bf16" else None, C.byref(z8) if z8 is not None else None,
-                                   _ptr(ws), ws.numel(), _stream(stream, dev)))
+        check(lib.prism_linear_fwd(C.byref(l), _addr(X), ldx, _addr(W), _addr(bias), _addr(residual), ldr, _addr(Y), ldy,
+                                   _addr(Z) if save == "bf16" else None, C.byref(z8) if z8 is not None else None,
+                                   _addr(ws), ws.numel(), _handle(stream, dev)))
     return LinearResult(Y, Z, ws)
 
 
@@ -635,17 +661,17 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
         named.append(("ws", ws))
     dev = _check_devices(named)
     lib = _lib.load()
-    with torch.cuda.device(dev):
+    with _on(dev):
         dX, dW, db = (None if name not in need else
                       t if t is not None else torch.empty(want[name][0], dtype=want[name][1], device=dev)
                       for name, t in zip(("dX", "dW", "db"), out))
         l = PrismLinear(n, cin, cout, act)
-        ws = ws if ws is not None else _workspace(lib.prism_linear_workspace_size(C.byref(l), 1), dev)
+        ws = ws if ws is not None else _workspace(lib.prism_linear_workspace_size(C.byref(l), 2 if isinstance(X, Ckpt8) else 1), dev)
         x8 = X.c_struct() if isinstance(X, Ckpt8) else None
         z8 = Z.c_struct() if isinstance(Z, Ckpt8) else None
-        check(lib.prism_linear_bwd(C.byref(l), _ptr(dY), lddy, None if x8 is not None else _ptr(X), ldx,
-                                   C.byref(x8) if x8 is not None else None, _ptr(W),
-                                   None if z8 is not None else _ptr(Z), ldz,
-                                   C.byref(z8) if z8 is not None else None, _ptr(dX), _ptr(dW), _ptr(db),
-                                   int(bool(grad_fp32)), _ptr(ws), ws.numel(), _stream(stream, dev)))
+        check(lib.prism_linear_bwd(C.byref(l), _addr(dY), lddy, None if x8 is not None else _addr(X), ldx,
+                                   C.byref(x8) if x8 is not None else None, _addr(W),
+                                   None if z8 is not None else _addr(Z), ldz,
+                                   C.byref(z8) if z8 is not None else None, _addr(dX), _addr(dW), _addr(db),
+                                   int(bool(grad_fp32)), _addr(ws), ws.numel(), _handle(stream, dev)))
     return LinearGrads(dX, dW, db, ws)

@@ -21,29 +21,24 @@ constexpr int kUnroll = 4;
 //   silu = z p(z):             slope p + z p (1 - p)
 //   gelu (tanh form) = z p(v), v = 2 sqrt(2/pi) (z + 0.044715 z^3): slope
 //                              p + z p (1 - p) v'
-// z is clamped where p is 0 or 1 to the last bit (e^-v overflows or vanishes), so
-// that no product of infinity and zero arises.  A NaN stays one (a restored
-// checkpoint block that held a non-finite value).
-__device__ __forceinline__ float clamp_nan(float x, float far) {
-  float y;
-  asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, t, %3;\n\t}" : "=f"(y) : "f"(x), "f"(far), "f"(-far));
-  return y;
-}
+// Far out p is 0 or 1 to the last bit (e^-v overflows or vanishes) and the second
+// term 0, as long as v' stays finite; it is held at 3e38.  A NaN stays one (a
+// restored checkpoint block that held a non-finite value).
 template <int ACT>
 __device__ __forceinline__ float2 act_slope(float2 z) {
   if constexpr (ACT == PRISM_ACT_RELU)
     return make_float2(z.x > 0.f ? 1.f : (z.x != z.x ? z.x : 0.f), z.y > 0.f ? 1.f : (z.y != z.y ? z.y : 0.f));
-  constexpr float kFar = ACT == PRISM_ACT_SILU ? 100.f : 30.f;
   const float2 one = make_float2(1.f, 1.f);
-  const float2 c = make_float2(clamp_nan(z.x, kFar), clamp_nan(z.y, kFar));
   if constexpr (ACT == PRISM_ACT_SILU) {
-    const float2 p = gemm::logistic2(fmul2(c, make_float2(-gemm::kLog2e, -gemm::kLog2e)));
-    return ffma2(fmul2(c, p), fsub2(one, p), p);
+    const float2 p = gemm::logistic2(fmul2(z, make_float2(-gemm::kLog2e, -gemm::kLog2e)));
+    return ffma2(fmul2(z, p), fsub2(one, p), p);
   } else {
     constexpr float k = gemm::kGelu2;
-    const float2 z2 = fmul2(c, c);
-    const float2 p = gemm::logistic2(fmul2(c, ffma2(z2, -0.044715f * k * gemm::kLog2e, -k * gemm::kLog2e)));
-    return ffma2(fmul2(fmul2(c, p), fsub2(one, p)), ffma2(z2, 0.134145f * k, k), p);
+    const float2 z2 = fmul2(z, z);
+    const float2 p = gemm::logistic2(fmul2(z, ffma2(z2, -0.044715f * k * gemm::kLog2e, -k * gemm::kLog2e)));
+    float2 dv = ffma2(z2, 0.134145f * k, k);
+    dv = make_float2(fminf(dv.x, 3e38f), fminf(dv.y, 3e38f));
+    return ffma2(fmul2(fmul2(z, p), fsub2(one, p)), dv, p);
   }
 }
 
@@ -56,6 +51,7 @@ struct Src {
   const uint8_t *scales;
   long long ldq;
   uint4 *dZ;  // [n][cols]
+  int *status;
 };
 
 // tx threads (a power of two, 8..32) cover 8 * tx columns of a row
@@ -63,36 +59,45 @@ template <int ACT, bool Z8>
 __global__ void __launch_bounds__(kThreads)
     act_grad_kernel(const Src s, long long n, int vecs, int tx, long long rows_per, float *__restrict__ part) {
   __shared__ float red[kThreads][9];
+  gemm::reset_status(s.status, 1);
   const int cx = threadIdx.x & (tx - 1), ry = threadIdx.x / tx, rows_step = kThreads / tx;
   const int cv = blockIdx.x * tx + cx;
-  const long long r0 = (long long)blockIdx.y * rows_per;
-  const long long r1 = r0 + rows_per < n ? r0 + rows_per : n;
+  const long long r0 = (long long)blockIdx.y * rows_per + ry;
+  const long long r1 = min((long long)(blockIdx.y + 1) * rows_per, n);
   float2 sum[4] = {};
-  if (cv < vecs) {
-    for (long long r = r0 + ry; r < r1; r += (long long)rows_step * kUnroll) {
+  if (cv < vecs && r0 < r1) {
+    int left = (int)((r1 - r0 + rows_step - 1) / rows_step);  // rows of this thread
+    const uint4 *dy = s.dY + r0 * s.ldy_vec + cv;
+    const uint4 *zp = (ACT != PRISM_ACT_NONE && !Z8) ? s.Z + r0 * s.ldz_vec + cv : nullptr;
+    const uint2 *qp = Z8 ? s.codes + r0 * (s.ldq >> 3) + cv : nullptr;
+    const uint8_t *sp = Z8 ? s.scales + r0 * (s.ldq >> 5) + (cv >> 2) : nullptr;
+    uint4 *dz = s.dZ + r0 * vecs + cv;
+    const long long dy_step = rows_step * s.ldy_vec, z_step = rows_step * s.ldz_vec, q_step = rows_step * (s.ldq >> 3),
+                    s_step = rows_step * (s.ldq >> 5), dz_step = (long long)rows_step * vecs;
+    for (; left > 0; left -= kUnroll) {
       uint4 d[kUnroll], z[kUnroll];
       uint32_t sc[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const long long rr = r + (long long)u * rows_step;
-        if (rr < r1) {
-          d[u] = ACT != PRISM_ACT_NONE ? __ldcs(s.dY + rr * s.ldy_vec + cv) : __ldg(s.dY + rr * s.ldy_vec + cv);
-          if constexpr (ACT != PRISM_ACT_NONE) {
-            if constexpr (Z8) {
-              const uint2 q = __ldcs(s.codes + rr * (s.ldq >> 3) + cv);
-              z[u].x = q.x;
-              z[u].y = q.y;
-              sc[u] = __ldg(s.scales + rr * (s.ldq >> 5) + (cv >> 2));
-            } else {
-              z[u] = __ldcs(s.Z + rr * s.ldz_vec + cv);
-            }
+        if (u < left) {
+          d[u] = __ldcs(dy);
+          dy += dy_step;
+          if constexpr (Z8) {
+            const uint2 q = __ldcs(qp);
+            z[u].x = q.x;
+            z[u].y = q.y;
+            sc[u] = __ldg(sp);
+            qp += q_step;
+            sp += s_step;
+          } else if constexpr (ACT != PRISM_ACT_NONE) {
+            z[u] = __ldcs(zp);
+            zp += z_step;
           }
         }
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const long long rr = r + (long long)u * rows_step;
-        if (rr >= r1) break;
+        if (u >= left) break;
         const uint32_t dw[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
         if constexpr (ACT != PRISM_ACT_NONE) {
           uint4 zz = z[u];
@@ -110,7 +115,8 @@ __global__ void __launch_bounds__(kThreads)
             sum[k] = fadd2(sum[k], g);
             o[k] = pack_bf16(g.x, g.y);
           }
-          s.dZ[rr * vecs + cv] = make_uint4(o[0], o[1], o[2], o[3]);
+          *dz = make_uint4(o[0], o[1], o[2], o[3]);
+          dz += dz_step;
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k) sum[k] = fadd2(sum[k], make_float2(bf16lo(dw[k]), bf16hi(dw[k])));
@@ -200,7 +206,7 @@ size_t act_grad_part_bytes(long long n, int cols) {
 
 cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, long long ldy, const uint16_t *Z,
                             long long ldz, const prism_ckpt8_t *Z8, uint16_t *dZ, float *part, void *db, int db_fp32,
-                            cudaStream_t st) {
+                            int *status, cudaStream_t st) {
   const actg::Shape sh = actg::shape_of(n, cols);
   actg::Src s;
   s.dY = reinterpret_cast<const uint4 *>(dY);
@@ -211,6 +217,7 @@ cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, 
   s.scales = Z8 ? Z8->scales : nullptr;
   s.ldq = Z8 ? Z8->ld : 0;
   s.dZ = reinterpret_cast<uint4 *>(dZ);
+  s.status = status;
   const dim3 grid(sh.strips, sh.blocks);
   const actg::Launch l{s, grid, n, cols / 8, sh.tx, sh.rows_per, db ? part : nullptr, st};
   switch (act) {

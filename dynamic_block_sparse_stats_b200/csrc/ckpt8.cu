@@ -3,9 +3,11 @@
 // between its forward and its backward.
 //
 // HBM-bound, one pass: pack reads 2 bytes and writes 33/32 bytes per value,
-// unpack the reverse.  Sixteen lanes own 128 channels of a row: each lane holds
-// eight (one 16-byte vector), four lanes share a block's maximum by shuffles,
-// and lane 0 of the sixteen writes their four scales as one word.
+// unpack the reverse.  Sixteen lanes own 128 channels of a row (a group): each
+// lane holds eight (one 16-byte vector), four lanes share a block's maximum by
+// shuffles, and lane 0 of the sixteen writes their four scales as one word.
+// What had to go to reach the memory's rate was integer work: rows are found by
+// stepping (one division per thread), the maximum is taken on pairs of bf16 bits.
 #include <algorithm>
 #include <cstdio>
 
@@ -18,48 +20,63 @@ namespace ck8 {
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // 128-channel groups in flight per half-warp
 
-__device__ __forceinline__ void unpack8(const uint4 &x, float (&v)[8]) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    v[2 * k] = bf16lo(w[k]);
-    v[2 * k + 1] = bf16hi(w[k]);
+// Groups 0 .. groups-1, gpr to a row; a half-warp takes every nhalf-th.  Its
+// place (row, group of the row) moves by (row_step, col_step), nhalf divided by gpr.
+struct Walk {
+  long long groups, nhalf, row_step;
+  int gpr, col_step;
+};
+struct Place {
+  long long g, row;
+  int col;
+  __device__ __forceinline__ Place(const Walk &w, long long start) : g(start), row(start / w.gpr) {
+    col = (int)(start - row * w.gpr);
   }
-}
+  __device__ __forceinline__ void step(const Walk &w) {
+    g += w.nhalf;
+    row += w.row_step;
+    col += w.col_step;
+    if (col >= w.gpr) {
+      col -= w.gpr;
+      ++row;
+    }
+  }
+};
 
-// groups: n * gpr groups of 128 channels, row-major; vec: 16-byte vectors of a
-// row that exist (the rest of the last group is zero)
+// vec: 16-byte vectors of a row that exist (the rest of the last group is zero)
 __global__ void __launch_bounds__(kThreads)
-    pack_kernel(const uint4 *__restrict__ x, long long ld_vec, int vec, long long groups, int gpr,
-                uint2 *__restrict__ codes, uint32_t *__restrict__ scales) {
+    pack_kernel(const uint4 *__restrict__ x, long long ld_vec, int vec, const Walk w, uint2 *__restrict__ codes,
+                uint32_t *__restrict__ scales) {
   const int l16 = threadIdx.x & 15;
-  const long long half = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 4;
-  const long long nhalf = ((long long)gridDim.x * kThreads) >> 4;
+  Place p(w, ((long long)blockIdx.x * kThreads + threadIdx.x) >> 4);
   // both half-warps of a warp run the same number of iterations (shuffles)
-  for (long long g0 = half & ~1LL; g0 < groups; g0 += nhalf * kUnroll) {
+  while (__any_sync(0xffffffffu, p.g < w.groups)) {
     uint4 in[kUnroll];
+    long long g[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const long long g = g0 + (half & 1) + u * nhalf;
+      const int c = p.col * 16 + l16;
+      g[u] = p.g;
       in[u] = make_uint4(0, 0, 0, 0);
-      if (g < groups) {
-        const long long row = g / gpr;
-        const int c = (int)(g - row * gpr) * 16 + l16;
-        if (c < vec) in[u] = __ldcs(x + row * ld_vec + c);
-      }
+      if (p.g < w.groups && c < vec) in[u] = __ldcs(x + p.row * ld_vec + c);
+      p.step(w);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const long long g = g0 + (half & 1) + u * nhalf;
-      float v[8];
-      unpack8(in[u], v);
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t h[4] = {in[u].x, in[u].y, in[u].z, in[u].w};
+      // magnitudes of the pairs; a NaN's bits compare above infinity's
+      uint32_t m = __vmaxu2(__vmaxu2(h[0] & 0x7fff7fffu, h[1] & 0x7fff7fffu), __vmaxu2(h[2] & 0x7fff7fffu, h[3] & 0x7fff7fffu));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const uint32_t top = max(m << 16, m & 0xffff0000u);
       const uint32_t s = ckpt8_scale(top);
       const float inv = ckpt8_inverse(s);
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] = bf16lo(h[k]);
+        v[2 * k + 1] = bf16hi(h[k]);
+      }
       if (top > kCkptTop) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = s == kCkptBad ? 0.f : ckpt8_clamp(v[k]);
@@ -67,51 +84,56 @@ __global__ void __launch_bounds__(kThreads)
       uint32_t sw = s << (8 * (l16 >> 2));
       sw |= __shfl_xor_sync(0xffffffffu, sw, 4);
       sw |= __shfl_xor_sync(0xffffffffu, sw, 8);
-      if (g < groups) {
-        codes[g * 16 + l16] =
-            make_uint2(ckpt8_code4(v[0], v[1], v[2], v[3], inv), ckpt8_code4(v[4], v[5], v[6], v[7], inv));
-        if (l16 == 0) scales[g] = sw;
+      if (g[u] < w.groups) {
+        __stcs(codes + g[u] * 16 + l16,
+               make_uint2(ckpt8_code4(v[0], v[1], v[2], v[3], inv), ckpt8_code4(v[4], v[5], v[6], v[7], inv)));
+        if (l16 == 0) scales[g[u]] = sw;
       }
     }
   }
 }
 
 __global__ void __launch_bounds__(kThreads)
-    unpack_kernel(const uint2 *__restrict__ codes, const uint8_t *__restrict__ scales, long long groups, int gpr,
-                  int vec, uint4 *__restrict__ x, long long ld_vec) {
+    unpack_kernel(const uint2 *__restrict__ codes, const uint8_t *__restrict__ scales, const Walk w, int vec,
+                  uint4 *__restrict__ x, long long ld_vec) {
   const int l16 = threadIdx.x & 15;
-  const long long half = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 4;
-  const long long nhalf = ((long long)gridDim.x * kThreads) >> 4;
-  for (long long g0 = half; g0 < groups; g0 += nhalf * kUnroll) {
+  Place p(w, ((long long)blockIdx.x * kThreads + threadIdx.x) >> 4);
+  while (p.g < w.groups) {
     uint2 q[kUnroll];
     uint32_t s[kUnroll];
+    uint4 *dst[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const long long g = g0 + u * nhalf;
-      if (g < groups) {
-        q[u] = __ldcs(codes + g * 16 + l16);
-        s[u] = __ldcs(scales + g * 4 + (l16 >> 2));
+      const int c = p.col * 16 + l16;
+      dst[u] = nullptr;
+      if (p.g < w.groups) {
+        q[u] = __ldcs(codes + p.g * 16 + l16);
+        s[u] = __ldcs(scales + p.g * 4 + (l16 >> 2));
+        if (c < vec) dst[u] = x + p.row * ld_vec + c;
       }
+      p.step(w);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const long long g = g0 + u * nhalf;
-      if (g >= groups) break;
-      const long long row = g / gpr;
-      const int c = (int)(g - row * gpr) * 16 + l16;
+      if (!dst[u]) continue;
       const uint32_t s2 = ckpt8_scale2(s[u]);
-      if (c < vec)
-        __stcs(x + row * ld_vec + c,
-               make_uint4(ckpt8_restore2(q[u].x, 0x4140, s2), ckpt8_restore2(q[u].x, 0x4342, s2),
-                          ckpt8_restore2(q[u].y, 0x4140, s2), ckpt8_restore2(q[u].y, 0x4342, s2)));
+      __stcs(dst[u], make_uint4(ckpt8_restore2(q[u].x, 0x4140, s2), ckpt8_restore2(q[u].x, 0x4342, s2),
+                                ckpt8_restore2(q[u].y, 0x4140, s2), ckpt8_restore2(q[u].y, 0x4342, s2)));
     }
   }
 }
 
 // one iteration of kUnroll groups per half-warp, or full occupancy
-int grid_for(long long groups) {
+Walk walk_for(long long n, long long ld, int &grid) {
+  Walk w;
+  w.gpr = (int)(ld / 128);
+  w.groups = n * w.gpr;
   const long long per_cta = (long long)(kThreads / 16) * kUnroll;
-  return (int)std::min<long long>((groups + per_cta - 1) / per_cta, (long long)device_sm_count() * 8);
+  grid = (int)std::min<long long>((w.groups + per_cta - 1) / per_cta, (long long)device_sm_count() * 8);
+  w.nhalf = (long long)grid * (kThreads / 16);
+  w.row_step = w.nhalf / w.gpr;
+  w.col_step = (int)(w.nhalf % w.gpr);
+  return w;
 }
 
 int check(const char *who, const uint16_t *x, int64_t n, int32_t width, int64_t ld, const prism_ckpt8_t *c) {
@@ -132,9 +154,7 @@ int check(const char *who, const uint16_t *x, int64_t n, int32_t width, int64_t 
   return report_error(PRISM_ERR_INVALID_ARG, msg);
 }
 
-int finish(const char *who) {
-  count_launches(1);
-  const cudaError_t e = cudaGetLastError();
+int finish(const char *who, cudaError_t e) {
   if (e != cudaSuccess) {
     char msg[256];
     snprintf(msg, sizeof(msg), "%s: %s", who, cudaGetErrorString(e));
@@ -145,6 +165,17 @@ int finish(const char *who) {
 }
 
 }  // namespace ck8
+
+cudaError_t launch_ckpt8_unpack(const prism_ckpt8_t &in, long long n, int width, uint16_t *x, long long ld,
+                                cudaStream_t st) {
+  int grid;
+  const ck8::Walk w = ck8::walk_for(n, in.ld, grid);
+  ck8::unpack_kernel<<<grid, ck8::kThreads, 0, st>>>(reinterpret_cast<const uint2 *>(in.codes), in.scales, w, width / 8,
+                                                     reinterpret_cast<uint4 *>(x), ld / 8);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
 }  // namespace prism
 
 using namespace prism;
@@ -159,12 +190,13 @@ extern "C" int prism_ckpt8_pack(const uint16_t *x, int64_t n, int32_t width, int
     return PRISM_OK;
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int gpr = (int)(out->ld / 128);
-  const long long groups = (long long)n * gpr;
-  ck8::pack_kernel<<<ck8::grid_for(groups), ck8::kThreads, 0, st>>>(
-      reinterpret_cast<const uint4 *>(x), (long long)(ld / 8), width / 8, groups, gpr,
-      reinterpret_cast<uint2 *>(out->codes), reinterpret_cast<uint32_t *>(out->scales));
-  return ck8::finish("prism_ckpt8_pack");
+  int grid;
+  const ck8::Walk w = ck8::walk_for(n, out->ld, grid);
+  ck8::pack_kernel<<<grid, ck8::kThreads, 0, st>>>(reinterpret_cast<const uint4 *>(x), (long long)(ld / 8), width / 8, w,
+                                                   reinterpret_cast<uint2 *>(out->codes),
+                                                   reinterpret_cast<uint32_t *>(out->scales));
+  count_launches(1);
+  return ck8::finish("prism_ckpt8_pack", cudaGetLastError());
 }
 
 extern "C" int prism_ckpt8_unpack(const prism_ckpt8_t *in, int64_t n, int32_t width, uint16_t *x, int64_t ld,
@@ -176,11 +208,5 @@ extern "C" int prism_ckpt8_unpack(const prism_ckpt8_t *in, int64_t n, int32_t wi
     clear_error();
     return PRISM_OK;
   }
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int gpr = (int)(in->ld / 128);
-  const long long groups = (long long)n * gpr;
-  ck8::unpack_kernel<<<ck8::grid_for(groups), ck8::kThreads, 0, st>>>(
-      reinterpret_cast<const uint2 *>(in->codes), in->scales, groups, gpr, width / 8, reinterpret_cast<uint4 *>(x),
-      (long long)(ld / 8));
-  return ck8::finish("prism_ckpt8_unpack");
+  return ck8::finish("prism_ckpt8_unpack", launch_ckpt8_unpack(*in, n, width, x, ld, reinterpret_cast<cudaStream_t>(stream)));
 }

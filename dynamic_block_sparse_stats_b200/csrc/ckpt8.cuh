@@ -41,10 +41,9 @@ __device__ __forceinline__ float ckpt8_clamp(float x) {
 // four codes in a word: x * inv + 1.5 * 2^23 rounds x * inv (exact: a power of
 // two) to an integer, whose two's complement stands in the low bits
 __device__ __forceinline__ uint32_t ckpt8_code4(float a, float b, float c, float d, float inv) {
-  const float m = 12582912.f;
-  const uint32_t ia = __float_as_uint(fmaf(a, inv, m)), ib = __float_as_uint(fmaf(b, inv, m));
-  const uint32_t ic = __float_as_uint(fmaf(c, inv, m)), id = __float_as_uint(fmaf(d, inv, m));
-  return __byte_perm(__byte_perm(ia, ib, 0x0040), __byte_perm(ic, id, 0x0040), 0x5410);
+  const float2 lo = ffma2(make_float2(a, b), inv, 12582912.f), hi = ffma2(make_float2(c, d), inv, 12582912.f);
+  return __byte_perm(__byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x0040),
+                     __byte_perm(__float_as_uint(hi.x), __float_as_uint(hi.y), 0x0040), 0x5410);
 }
 
 // one block held by one thread: returns s, codes in q

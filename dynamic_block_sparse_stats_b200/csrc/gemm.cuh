@@ -158,7 +158,20 @@ struct Args {
   long long b_ld;
   int k_total;
   int *status;
+  int reset;  // the call's first kernel: clear the status word
+  // split_kernel stores without tensor maps
+  const uint16_t *R;
+  long long ldr;
+  void *Y;
+  long long ldy;
+  uint16_t *Z;
+  int out_fp32;
 };
+// The status word starts at 0 with the call's first kernel: cleared by its first
+// block, seconds before the shortest wait of any block can run out.
+__device__ __forceinline__ void reset_status(int *status, int reset) {
+  if (reset && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) status[0] = status[1] = 0;
+}
 
 // ---------------------------------------------------------------------------
 // cluster helpers
@@ -171,11 +184,17 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// the same shared-memory location in CTA 0 of the cluster
-__device__ __forceinline__ uint32_t map_to_cta0(const void *p) {
+// the same shared-memory location in another CTA of the cluster
+__device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, int cta) {
   uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
   return r;
+}
+__device__ __forceinline__ uint32_t map_to_cta0(const void *p) { return map_to_cta(smem_u32(p), 0); }
+__device__ __forceinline__ float4 load_cta(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
 }
 // Arrive on CTA 0's barrier.  What it publishes is not read through the generic
 // proxy by CTA 0: accumulators have been read (tcgen05.wait::ld), or this CTA's
@@ -321,6 +340,45 @@ __device__ __forceinline__ uint4 pack8(const float2 (&v)[16], int i) {
                     pack_bf16(v[i + 3].x, v[i + 3].y));
 }
 
+// 32 columns of a row, from column c0
+__device__ __forceinline__ void add_bias(float2 (&v)[16], const uint16_t *bias, int c0, int cols) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (c0 + i * 8 < cols) {
+      const uint4 b = __ldg(reinterpret_cast<const uint4 *>(bias + c0) + i);
+      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[4 * i + k] = fadd2(v[4 * i + k], bf16_pair(w[k]));
+    }
+  }
+}
+__device__ __forceinline__ void apply_act(float2 (&v)[16], int act) {
+  switch (act) {
+    case PRISM_ACT_RELU:
+      act32<PRISM_ACT_RELU>(v);
+      break;
+    case PRISM_ACT_SILU:
+      act32<PRISM_ACT_SILU>(v);
+      break;
+    case PRISM_ACT_GELU:
+      act32<PRISM_ACT_GELU>(v);
+      break;
+    default:
+      break;
+  }
+}
+// the block's checkpoint; returns its scale byte
+__device__ __forceinline__ uint32_t save_codes(const float2 (&v)[16], const Args &args, int row, int c0) {
+  uint32_t q[8];
+  const uint32_t sc = ckpt8_quantise(v, q);
+  if (row < args.rows && c0 < args.ldq) {
+    uint4 *dst = reinterpret_cast<uint4 *>(args.codes + (long long)row * args.ldq + c0);
+    dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
+    dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
+  }
+  return sc;
+}
+
 // one warp's 32 x 32 fp32 values (thread = row) through a staging buffer to
 // column x, row y of `map`
 __device__ __forceinline__ void stage_fp32(const CUtensorMap *map, uint8_t *buf, const uint32_t (&v)[32], int lane, int x,
@@ -437,44 +495,15 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
           float2 v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-          if (args.bias) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (cg0 + i * 8 < args.cols) {
-                const uint4 b = __ldg(reinterpret_cast<const uint4 *>(args.bias + cg0) + i);
-                const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[4 * i + k] = fadd2(v[4 * i + k], bf16_pair(w[k]));
-              }
-            }
-          }
+          if (args.bias) add_bias(v, args.bias, cg0, args.cols);
           if (z16) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4 *>(row + kStageBuf + (((g * 4 + i) ^ sw) << 4)) = pack8(v, 4 * i);
           } else if (args.save_z == 2) {
-            uint32_t q[8];
-            const uint32_t sc = ckpt8_quantise(v, q);
-            if (m0 + lane < args.rows && cg0 < args.ldq) {
-              uint4 *dst = reinterpret_cast<uint4 *>(args.codes + (long long)(m0 + lane) * args.ldq + cg0);
-              dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
-              dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
-            }
-            scale2 |= sc << (8 * g);
+            scale2 |= save_codes(v, args, m0 + lane, cg0) << (8 * g);
           }
-          switch (args.act) {
-            case PRISM_ACT_RELU:
-              act32<PRISM_ACT_RELU>(v);
-              break;
-            case PRISM_ACT_SILU:
-              act32<PRISM_ACT_SILU>(v);
-              break;
-            case PRISM_ACT_GELU:
-              act32<PRISM_ACT_GELU>(v);
-              break;
-            default:
-              break;
-          }
+          apply_act(v, args.act);
           if (res && g == 0) {
             ok = __all_sync(0xffffffffu, mbar_wait(&bar.res[ew][yb], (res_phase >> yb) & 1, status, 408));
             res_phase ^= 1u << yb;
@@ -595,6 +624,7 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
   const int group = blockIdx.x / CG;
   const Sched &s = args.s;
   int *status = args.status;
+  reset_status(status, args.reset);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 6; ++i) {
@@ -830,6 +860,217 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
     tc_fence_after();
     tmem_dealloc_g<CG>(tmem, C::TMEM_COLS);
   }
+}
+
+// ---------------------------------------------------------------------------
+// few tiles: the contraction split over a cluster
+// ---------------------------------------------------------------------------
+// When the output has fewer tiles than the GPU has SMs (few tokens, or a small
+// weight), a cluster of up to eight CTAs shares one 128 x 64 tile: each walks
+// its part of the contraction and leaves its fp32 partial tile in its own shared
+// memory.  After a cluster barrier every thread of the cluster sums its pieces of
+// four columns, in the order of the CTAs, over distributed shared memory, and
+// finishes them.  One launch, no partial sums in HBM, the same bits every time.
+//
+// SWAP: up to 64 tokens, as the 64-wide operand B, with the weight's channels as
+// the 128 rows: a stage then brings 128 rows of the weight instead of 128 rows
+// of mostly absent tokens.
+struct SplitBars {
+  uint64_t full[4], empty[4], acc_full, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+struct SplitSmem {
+  static constexpr int NST = 4;
+  static constexpr int A_BYTES = 128 * BK * 2, B_BYTES = 64 * BK * 2, STAGE = A_BYTES + B_BYTES;
+  static constexpr int OFF_BAR = NST * STAGE;
+  static constexpr int SMEM = OFF_BAR + 256 + 1024;  // slack to align the base to 1024
+  static_assert(128 * 64 * 4 <= NST * STAGE, "the partial tile takes the stages' place");
+  static_assert(sizeof(SplitBars) <= 256, "barrier space");
+};
+
+template <bool A_MN, bool B_MN, bool SWAP>
+__global__ void __launch_bounds__(256, 2)
+    split_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB, const Args args,
+                 int split) {
+  using L = SplitSmem;
+  constexpr int NST = L::NST;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  SplitBars &bar = *reinterpret_cast<SplitBars *>(smem + L::OFF_BAR);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
+  const int m0 = (tile / args.s.tiles_n) * 128, n0 = (tile % args.s.tiles_n) * 64;
+  const int k0 = (int)((long long)args.s.kc * rank / split), k1 = (int)((long long)args.s.kc * (rank + 1) / split);
+  int *status = args.status;
+  reset_status(status, args.reset);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    mbar_init(&bar.acc_full, 1);
+    mbar_init(&bar.drain, 1);
+    bar.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 2) tmem_alloc_g<1>(&bar.tmem_base, 64);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem_base;
+
+  if (warp == 0 && lane == 0) {
+    bool ok = true;
+    int j = 0;
+    for (int k = k0; k < k1; ++k, ++j) {
+      const int st = j % NST;
+      if (j >= NST && !(ok = mbar_wait(&bar.empty[st], ((j / NST) - 1) & 1, status, 421))) break;
+      if (*reinterpret_cast<volatile int *>(&bar.abort)) {
+        ok = false;
+        break;
+      }
+      uint8_t *a = smem + st * L::STAGE, *b = a + L::A_BYTES;
+      mbar_arrive_expect_tx(&bar.full[st], L::STAGE);
+      if constexpr (A_MN) {
+        tma_load_2d(a, &mapA, &bar.full[st], m0, k * BK);
+        tma_load_2d(a + BK * 128, &mapA, &bar.full[st], m0 + 64, k * BK);
+      } else {
+        tma_load_2d(a, &mapA, &bar.full[st], k * BK, m0);
+      }
+      if constexpr (B_MN)
+        tma_load_2d(b, &mapB, &bar.full[st], n0, k * BK);
+      else
+        tma_load_2d(b, &mapB, &bar.full[st], k * BK, n0);
+    }
+    if (!ok) bar.abort = 1;
+    drain_loads(bar.full, NST, j, status, 422);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_bf16(128, 64, B_MN ? 1 : 0) | (A_MN ? 1u << 15 : 0u);
+    bool ok = true;
+    int j = 0;
+    for (int k = k0; k < k1; ++k, ++j) {
+      const int st = j % NST;
+      if (!(ok = mbar_wait(&bar.full[st], (j / NST) & 1, status, 423))) break;
+      tc_fence_after();
+      const uint32_t a = smem_u32(smem + st * L::STAGE), b = a + L::A_BYTES;
+      const uint64_t da = A_MN ? sdesc_sw128(a, BK * 128, 1024) : sdesc_sw128(a, 16, 1024);
+      const uint64_t db = B_MN ? sdesc_sw128(b, BK * 128, 1024) : sdesc_sw128(b, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < BK / 16; ++kk)
+        mma_ss(tmem, da + (A_MN ? (uint64_t)kk * 128 : kslice16(kk, 0)), db + (B_MN ? (uint64_t)kk * 128 : kslice16(kk, 0)),
+               idesc, (j > 0 || kk > 0) ? 1u : 0u);
+      mma_commit(&bar.empty[st]);
+    }
+    if (ok) {
+      mma_commit(&bar.acc_full);
+    } else {
+      bar.abort = 1;
+      mma_drain(&bar.drain, status, 424);
+    }
+  } else if (warp >= 4) {
+    // partial tile -> shared memory as [output row][output column]: plain, row-per-thread 16-byte units swizzled by
+    // the row; swapped, a thread holds an output column, and neighbours' words are neighbours
+    const int row = (warp & 3) * 32 + lane;
+    if (__all_sync(0xffffffffu, mbar_wait(&bar.acc_full, 0, status, 425))) {
+      tc_fence_after();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t v[32];
+        tmem_ld32(tmem + g * 32 + ((uint32_t)((warp & 3) * 32) << 16), v);
+        tmem_wait_ld();
+        if constexpr (SWAP) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) *reinterpret_cast<uint32_t *>(smem + (g * 32 + i) * 512 + row * 4) = v[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4 *>(smem + row * 256 + (((g * 8 + i) ^ (row & 15)) << 4)) =
+                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+    } else {
+      bar.abort = 1;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc_g<1>(tmem, 64);
+  if (!*reinterpret_cast<volatile int *>(&bar.abort)) {
+    constexpr int UNITS = SWAP ? 32 : 16;  // four-column pieces of a row
+    const int om = SWAP ? n0 : m0, on = SWAP ? m0 : n0;  // the tile's place in the output
+#pragma unroll 1
+    for (int x = rank * 256 + threadIdx.x; x < 2048; x += 256 * split) {
+      const int r = x / UNITS, unit = x % UNITS;
+      const int m = om + r, c = on + unit * 4;
+      const uint32_t src = smem_u32(smem) + (SWAP ? r * 512 + unit * 16 : r * 256 + ((unit ^ (r & 15)) << 4));
+      float2 lo = make_float2(0.f, 0.f), hi = lo;
+#pragma unroll 8
+      for (int q = 0; q < split; ++q) {
+        const float4 p = load_cta(map_to_cta(src, q));
+        lo = fadd2(lo, make_float2(p.x, p.y));
+        hi = fadd2(hi, make_float2(p.z, p.w));
+      }
+      const bool in = m < args.rows && c < args.cols;
+      if (args.bias && c < args.cols) {
+        const uint2 b = __ldg(reinterpret_cast<const uint2 *>(args.bias + c));
+        lo = fadd2(lo, bf16_pair(b.x));
+        hi = fadd2(hi, bf16_pair(b.y));
+      }
+      if (args.save_z == 1 && in)
+        *reinterpret_cast<uint2 *>(args.Z + (long long)m * args.cols + c) =
+            make_uint2(pack_bf16(lo.x, lo.y), pack_bf16(hi.x, hi.y));
+      if (args.save_z == 2) {
+        // eight lanes hold a block
+        uint32_t top = max(max(__float_as_uint(lo.x) & 0x7fffffffu, __float_as_uint(lo.y) & 0x7fffffffu),
+                           max(__float_as_uint(hi.x) & 0x7fffffffu, __float_as_uint(hi.y) & 0x7fffffffu));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const uint32_t sc = ckpt8_scale(top);
+        const float inv = ckpt8_inverse(sc);
+        float2 a = lo, b = hi;
+        if (top > kCkptTop) {
+          const bool bad = sc == kCkptBad;
+          a = make_float2(bad ? 0.f : ckpt8_clamp(lo.x), bad ? 0.f : ckpt8_clamp(lo.y));
+          b = make_float2(bad ? 0.f : ckpt8_clamp(hi.x), bad ? 0.f : ckpt8_clamp(hi.y));
+        }
+        if (m < args.rows && c < args.ldq) {
+          *reinterpret_cast<uint32_t *>(args.codes + (long long)m * args.ldq + c) = ckpt8_code4(a.x, a.y, b.x, b.y, inv);
+          if (unit % 8 == 0) args.scales[(long long)m * (args.ldq / 32) + c / 32] = (uint8_t)sc;
+        }
+      }
+      if (!in) continue;
+      if (args.out_fp32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(args.Y) + (long long)m * args.ldy + c) =
+            make_float4(lo.x, lo.y, hi.x, hi.y);
+        continue;
+      }
+      switch (args.act) {
+        case PRISM_ACT_RELU:
+          lo = act_value<PRISM_ACT_RELU>(lo), hi = act_value<PRISM_ACT_RELU>(hi);
+          break;
+        case PRISM_ACT_SILU:
+          lo = act_value<PRISM_ACT_SILU>(lo), hi = act_value<PRISM_ACT_SILU>(hi);
+          break;
+        case PRISM_ACT_GELU:
+          lo = act_value<PRISM_ACT_GELU>(lo), hi = act_value<PRISM_ACT_GELU>(hi);
+          break;
+        default:
+          break;
+      }
+      if (args.R) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(args.R + (long long)m * args.ldr + c);
+        lo = fadd2(lo, bf16_pair(q.x));
+        hi = fadd2(hi, bf16_pair(q.y));
+      }
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(args.Y) + (long long)m * args.ldy + c) =
+          make_uint2(pack_bf16(lo.x, lo.y), pack_bf16(hi.x, hi.y));
+    }
+  }
+  cluster_sync_all();  // no CTA leaves while another reads its partial tile
 }
 
 }  // namespace gemm

@@ -103,11 +103,16 @@ cudaError_t make_map_2d(CUtensorMap *map, MapType type, const void *base, long l
                         int box_cols, int box_rows);
 
 // act_grad.cu: dZ = dY act'(Z) (nothing to write without an activation) and
-// db = its column sums, through `part` (act_grad_part_bytes; db may be NULL)
+// db = its column sums, through `part` (act_grad_part_bytes; db may be NULL); clears
+// the status word
 size_t act_grad_part_bytes(long long n, int cols);
 cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, long long ldy, const uint16_t *Z,
                             long long ldz, const prism_ckpt8_t *Z8, uint16_t *dZ, float *part, void *db, int db_fp32,
-                            cudaStream_t st);
+                            int *status, cudaStream_t st);
+
+// ckpt8.cu: x[n][ld] = the values of a checkpoint
+cudaError_t launch_ckpt8_unpack(const prism_ckpt8_t &in, long long n, int width, uint16_t *x, long long ld,
+                                cudaStream_t st);
 
 // SMs of the current device (148 where there is none)
 int device_sm_count();

@@ -4,6 +4,7 @@
 // matrix products), act_grad.cu (dZ and db).  Host side: checks, tile choice,
 // tensor maps.
 #include <algorithm>
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 
@@ -12,11 +13,13 @@
 namespace prism {
 
 int device_sm_count() {
+  static std::atomic<int> known[64];  // by device; a device's count never changes
   int dev = 0, c = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess &&
-      cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && c > 0)
-    return c;
-  return 148;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 64 && (c = known[dev].load(std::memory_order_relaxed)) > 0) return c;
+  if (cudaDeviceGetAttribute(&c, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || c <= 0) return 148;
+  if (dev < 64) known[dev].store(c, std::memory_order_relaxed);
+  return c;
 }
 
 namespace lin {
@@ -28,30 +31,41 @@ using gemm::Sched;
 // ---------------------------------------------------------------------------
 // tile choice
 // ---------------------------------------------------------------------------
-struct Tile {
-  int cg, bn;
-};
-// A stage's time on one CTA group, in SM clocks
-static double stage_cost(const Tile &t) { return t.cg == 2 ? (t.bn == 256 ? 512 : 384) : (t.bn == 128 ? 384 : 320); }
-
-static Sched make_sched(const Tile &t, int rows, int cols, int kc, bool split) {
+// Three ways to a matrix product, timed on this GPU (us; kc = 64-deep stages):
+//   pairs   256 x 256 tiles on CTA pairs, persistent: 0.40 a stage (power and L2
+//           bound, 80% of the tensor pipe), 6.0 around them
+//   single  128 x 128 tiles, persistent: 0.35 a stage (L2 bound), 4.2 around
+//   split   128 x 64 tiles, the contraction over up to 8 CTAs of a cluster: 0.33
+//           a stage, 5.0 around, one tile per cluster
+// The least estimate is taken.
+struct Plan {
+  int cg, bn;  // tile: 128 * cg rows, bn columns
+  int split;   // > 0: split_kernel with clusters of this size
+  bool swap;   // with the tokens as its 64-wide operand
   Sched s;
-  const int bm = 128 * t.cg;
-  s.tiles_n = (cols + t.bn - 1) / t.bn;
+  double us;
+};
+constexpr int kMaxSplit = 8;
+
+static Sched make_sched(int cg, int bn, int rows, int cols, int kc, bool share) {
+  Sched s;
+  const int bm = 128 * cg;
+  s.tiles_n = (cols + bn - 1) / bn;
   s.tiles = ((rows + bm - 1) / bm) * s.tiles_n;
   s.kc = kc;
   s.full = s.tiles;
   s.rem = 0;
   s.km = kc;
-  const int most = device_sm_count() / t.cg;
+  const int most = device_sm_count() / cg;
   s.groups = std::min(most, s.tiles);
-  if (split) {
+  if (share) {
     // at least 8 stages a group: below that the partial sums cost more than the products
     const long long want = std::max<long long>(s.tiles, (long long)s.tiles * kc / 8);
     s.groups = (int)std::min<long long>(most, want);
     const int rem = s.tiles % s.groups;
     const int km = (int)(((long long)kc * rem + s.groups - 1) / s.groups);
-    if (rem && km < kc) {
+    // every helper gets at least one stage of a tail
+    if (rem && km < kc && (long long)rem * (kc - km) >= s.groups - rem) {
       s.rem = rem;
       s.km = km;
       s.full = s.tiles - rem;
@@ -62,63 +76,101 @@ static Sched make_sched(const Tile &t, int rows, int cols, int kc, bool split) {
   return s;
 }
 
-static double sched_cost(const Tile &t, const Sched &s) {
-  const double tail = 2000.0;  // filling the pipeline and the last epilogue
-  const double waves = s.rem ? (double)s.full / s.groups + (double)s.rem / s.groups
-                             : (double)((s.tiles + s.groups - 1) / s.groups);
-  return waves * s.kc * stage_cost(t) + tail * t.bn / 256;
-}
-
-static Tile choose(const Tile *c, int n, int rows, int cols, int kc, bool split) {
-  Tile best = c[0];
-  double cost = 1e300;
-  for (int i = 0; i < n; ++i) {
-    const double x = sched_cost(c[i], make_sched(c[i], rows, cols, kc, split));
-    if (x < cost) {
-      cost = x;
-      best = c[i];
-    }
+// share: the tiles of the last wave may be divided (the weight gradient's);
+// chain: longest part of the contraction the split kernel may take in one sum
+static Plan make_plan(int rows, int cols, int kc, bool share, int chain, bool may_swap) {
+  Plan best = {};
+  best.us = 1e300;
+  const int sms = device_sm_count();
+  for (int big = 0; big < 2; ++big) {
+    Plan p = {};
+    p.cg = big ? 2 : 1;
+    p.bn = big ? 256 : 128;
+    p.s = make_sched(p.cg, p.bn, rows, cols, kc, share);
+    const double waves = p.s.rem ? (double)p.s.full / p.s.groups : (double)((p.s.tiles + p.s.groups - 1) / p.s.groups);
+    p.us = (big ? 6.0 : 4.2) + waves * kc * (big ? 0.40 : 0.35);
+    if (p.s.rem) p.us += p.s.km * (big ? 0.40 : 0.35) + 5.0;  // and the kernel that adds the parts
+    if (p.us < best.us) best = p;
+  }
+  Plan p = {};
+  p.cg = 1;
+  p.bn = 64;
+  p.swap = may_swap && rows <= 64;  // only ever true of a split plan
+  p.s = p.swap ? make_sched(1, 64, cols, rows, kc, false) : make_sched(1, 64, rows, cols, kc, false);
+  if (p.s.tiles <= sms) {
+    p.split = 1;
+    while (p.split < kMaxSplit && 2 * p.split * p.s.tiles <= sms && 2 * p.split <= kc) p.split *= 2;
+    const int part = (kc + p.split - 1) / p.split;
+    p.us = 5.0 + part * 0.33;
+    if (part <= chain && p.us < best.us) best = p;
   }
   return best;
 }
 
-static const Tile kTiles[] = {{2, 256}, {2, 128}, {1, 128}, {1, 64}};
-static const Tile kGradTiles[] = {{2, 256}, {1, 128}};
-
 // ---------------------------------------------------------------------------
 // partial sums of the weight gradient
 // ---------------------------------------------------------------------------
-// dW of the split tiles = their slots in a fixed order: first part, then the
-// helpers'.  One float4 per thread; 4 * 256 outputs per CTA.
+// dW of the split tiles = their slots in a fixed order: the first part, then the
+// helpers' parts.  Y rows of threads take every Y-th part each and meet in shared
+// memory, so that a small output cut into many parts (64 x 64 over 92160 tokens:
+// 149) is read by enough threads; a CTA owns 4096 / Y outputs.
+template <int Y>
 __global__ void __launch_bounds__(256)
     sum_parts_kernel(const float *__restrict__ part, const Sched s, int bm, int bn, int rows, int cols,
                      void *__restrict__ out, int fp32) {
-  const int t = blockIdx.y;
-  const int e = (blockIdx.x * 256 + threadIdx.x) * 4;
-  const int r = e / bn, c = e % bn;
+  constexpr int LANES = 256 / Y;
+  __shared__ float4 red[Y > 1 ? Y : 1][LANES];
+  const int t = blockIdx.y, lane = threadIdx.x % LANES, y = threadIdx.x / LANES;
   const int tile = s.full + t;
-  const int row = (tile / s.tiles_n) * bm + r, col = (tile % s.tiles_n) * bn + c;
-  if (r >= bm || row >= rows || col >= cols) return;
+  const int row0 = (tile / s.tiles_n) * bm, col0 = (tile % s.tiles_n) * bn;
   const long long slot = (long long)bm * bn;
-  float4 a = *reinterpret_cast<const float4 *>(part + t * slot + e);
-  const int tail = s.kc - s.km, helpers = s.groups - s.rem;
-  // the helpers whose ranges meet tile t's tail: their starts are rem * tail * h / helpers, rounded down
-  int h = max(0, (int)((long long)t * helpers / s.rem) - 1);
-  for (; h < helpers; ++h) {
-    const long long lo = gemm::helper_start(s, h), hi = gemm::helper_start(s, h + 1);
-    if (lo >= (long long)(t + 1) * tail) break;
-    if (hi <= (long long)t * tail || lo == hi) continue;
-    const float4 b = *reinterpret_cast<const float4 *>(part + (s.rem + h + t) * slot + e);
-    a.x += b.x;
-    a.y += b.y;
-    a.z += b.z;
-    a.w += b.w;
+  const long long lo = (long long)t * (s.kc - s.km), hi = lo + (s.kc - s.km);
+  const int helpers = s.groups - s.rem;
+  // the helpers [h0, h1) whose ranges meet tile t's tail: starts are rem * tail * h / helpers, rounded down
+  int h0 = max(0, (int)((long long)t * helpers / s.rem) - 1);
+  while (gemm::helper_start(s, h0 + 1) <= lo) ++h0;
+  int h1 = h0 + 1;
+  while (h1 < helpers && gemm::helper_start(s, h1) < hi) ++h1;
+  const float *first = part + t * slot, *more = part + (s.rem + h0 + t) * slot;
+  const int parts = 1 + h1 - h0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = ((blockIdx.x * 4 + i) * LANES + lane) * 4;
+    const int row = row0 + e / bn, col = col0 + e % bn;
+    const bool in = row < rows && col < cols;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) {
+#pragma unroll 4
+      for (int p = y; p < parts; p += Y) {
+        const float4 b = __ldcs(reinterpret_cast<const float4 *>((p == 0 ? first : more + (p - 1) * slot) + e));
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
+      }
+    }
+    if constexpr (Y > 1) {
+      if (i > 0) __syncthreads();
+      red[y][lane] = a;
+      __syncthreads();
+      if (y == 0) {
+#pragma unroll
+        for (int k = 1; k < Y; ++k) {
+          const float4 b = red[k][lane];
+          a.x += b.x;
+          a.y += b.y;
+          a.z += b.z;
+          a.w += b.w;
+        }
+      }
+    }
+    if (y > 0 || !in) continue;
+    const long long o = (long long)row * cols + col;
+    if (fp32)
+      *reinterpret_cast<float4 *>(static_cast<float *>(out) + o) = a;
+    else
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + o) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
   }
-  const long long o = (long long)row * cols + col;
-  if (fp32)
-    *reinterpret_cast<float4 *>(static_cast<float *>(out) + o) = a;
-  else
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + o) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
 }
 
 // ---------------------------------------------------------------------------
@@ -142,37 +194,51 @@ static cudaError_t rows_map(CUtensorMap *m, const void *base, long long cols, lo
   return make_map_2d(m, MAP_BF16, base, cols, rows, ld, 64, box_rows);
 }
 
-template <bool A_MN, bool B_MN>
-static cudaError_t launch_tile(const Tile &t, const Maps &m, const Args &args, cudaStream_t st) {
-  if (t.cg == 2) {
-    if (t.bn == 256) return launch<Cfg<2, 256, A_MN, B_MN>>(m, args, st);
-    return launch<Cfg<2, 128, A_MN, B_MN>>(m, args, st);
-  }
-  if (t.bn == 128) return launch<Cfg<1, 128, A_MN, B_MN>>(m, args, st);
-  return launch<Cfg<1, 64, A_MN, B_MN>>(m, args, st);
+template <bool A_MN, bool B_MN, bool SWAP = false>
+static cudaError_t launch_split(const Plan &p, const Maps &m, const Args &args, cudaStream_t st) {
+  const auto k = gemm::split_kernel<A_MN, B_MN, SWAP>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm::SplitSmem::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(p.s.tiles * p.split));
+  c.blockDim = dim3(256);
+  c.dynamicSmemBytes = gemm::SplitSmem::SMEM;
+  c.stream = st;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  e = cudaLaunchKernelEx(&c, k, m.a, m.b, args, p.split);
+  count_launches(1);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-template <bool B8, bool SUM>
-static cudaError_t launch_grad(const Tile &t, const Maps &m, const Args &args, cudaStream_t st) {
-  if (t.cg == 2) return launch<Cfg<2, 256, true, true, B8, SUM>>(m, args, st);
-  return launch<Cfg<1, 128, true, true, B8, SUM>>(m, args, st);
+template <bool A_MN, bool B_MN>
+static cudaError_t launch_plan(const Plan &p, const Maps &m, const Args &args, cudaStream_t st) {
+  if (p.split && p.swap) return launch_split<B_MN, A_MN, true>(p, m, args, st);
+  if (p.split) return launch_split<A_MN, B_MN>(p, m, args, st);
+  if (p.cg == 2) return launch<Cfg<2, 256, A_MN, B_MN>>(m, args, st);
+  return launch<Cfg<1, 128, A_MN, B_MN>>(m, args, st);
+}
+
+static Plan forward_plan(const prism_linear_t &l) {
+  return make_plan((int)l.n, l.out, (l.in + gemm::BK - 1) / gemm::BK, false, 1 << 30, true);
 }
 
 static cudaError_t forward(const prism_linear_t &l, const uint16_t *X, long long ldx, const uint16_t *W,
                            const uint16_t *bias, const uint16_t *R, long long ldr, uint16_t *Y, long long ldy,
                            uint16_t *Z, const prism_ckpt8_t *Z8, int *status, cudaStream_t st) {
-  const int rows = (int)l.n, cols = l.out, kc = (l.in + gemm::BK - 1) / gemm::BK;
-  const Tile t = choose(kTiles, 4, rows, cols, kc, false);
+  const int rows = (int)l.n, cols = l.out;
+  const Plan p = forward_plan(l);
   Maps m;
   cudaError_t e;
-  if ((e = rows_map(&m.a, X, l.in, rows, ldx, 128)) != cudaSuccess) return e;
-  if ((e = rows_map(&m.b, W, l.in, cols, l.in, t.bn / t.cg)) != cudaSuccess) return e;
-  if ((e = rows_map(&m.y, Y, cols, rows, ldy, 32)) != cudaSuccess) return e;
-  m.r = m.z = m.y;
-  if (R && (e = rows_map(&m.r, R, cols, rows, ldr, 32)) != cudaSuccess) return e;
-  if (Z && (e = rows_map(&m.z, Z, cols, rows, cols, 32)) != cudaSuccess) return e;
+  CUtensorMap &mx = p.swap ? m.b : m.a, &mw = p.swap ? m.a : m.b;
+  if ((e = rows_map(&mx, X, l.in, rows, ldx, p.swap ? 64 : 128)) != cudaSuccess) return e;
+  if ((e = rows_map(&mw, W, l.in, cols, l.in, p.swap ? 128 : p.bn / p.cg)) != cudaSuccess) return e;
   Args a = {};
-  a.s = make_sched(t, rows, cols, kc, false);
+  a.s = p.s;
   a.rows = rows;
   a.cols = cols;
   a.bias = bias;
@@ -185,78 +251,122 @@ static cudaError_t forward(const prism_linear_t &l, const uint16_t *X, long long
     a.ldq = Z8->ld;
   }
   a.status = status;
-  return launch_tile<false, false>(t, m, a, st);
+  a.reset = 1;
+  if (p.split) {
+    a.R = R;
+    a.ldr = ldr;
+    a.Y = Y;
+    a.ldy = ldy;
+    a.Z = Z;
+  } else {
+    if ((e = rows_map(&m.y, Y, cols, rows, ldy, 32)) != cudaSuccess) return e;
+    m.r = m.z = m.y;
+    if (R && (e = rows_map(&m.r, R, cols, rows, ldr, 32)) != cudaSuccess) return e;
+    if (Z && (e = rows_map(&m.z, Z, cols, rows, cols, 32)) != cudaSuccess) return e;
+  }
+  return launch_plan<false, false>(p, m, a, st);
 }
 
 // dX [n][in] = dZ [n][out] W [out][in]
 static cudaError_t input_grad(const prism_linear_t &l, const uint16_t *dZ, long long ldd, const uint16_t *W,
-                              uint16_t *dX, int *status, cudaStream_t st) {
-  const int rows = (int)l.n, cols = l.in, kc = (l.out + gemm::BK - 1) / gemm::BK;
-  const Tile t = choose(kTiles, 4, rows, cols, kc, false);
+                              uint16_t *dX, int *status, int reset, cudaStream_t st) {
+  const int rows = (int)l.n, cols = l.in;
+  const Plan p = make_plan(rows, cols, (l.out + gemm::BK - 1) / gemm::BK, false, 1 << 30, true);
   Maps m;
   cudaError_t e;
-  if ((e = rows_map(&m.a, dZ, l.out, rows, ldd, 128)) != cudaSuccess) return e;
-  if ((e = rows_map(&m.b, W, l.in, l.out, l.in, gemm::BK)) != cudaSuccess) return e;
-  if ((e = rows_map(&m.y, dX, cols, rows, cols, 32)) != cudaSuccess) return e;
-  m.r = m.z = m.y;
+  CUtensorMap &mz = p.swap ? m.b : m.a, &mw = p.swap ? m.a : m.b;
+  if ((e = rows_map(&mz, dZ, l.out, rows, ldd, p.swap ? 64 : 128)) != cudaSuccess) return e;
+  if ((e = rows_map(&mw, W, l.in, l.out, l.in, gemm::BK)) != cudaSuccess) return e;
   Args a = {};
-  a.s = make_sched(t, rows, cols, kc, false);
+  a.s = p.s;
   a.rows = rows;
   a.cols = cols;
   a.status = status;
-  return launch_tile<false, true>(t, m, a, st);
+  a.reset = reset;
+  if (p.split) {
+    a.Y = dX;
+    a.ldy = cols;
+  } else {
+    if ((e = rows_map(&m.y, dX, cols, rows, cols, 32)) != cudaSuccess) return e;
+    m.r = m.z = m.y;
+  }
+  return launch_plan<false, true>(p, m, a, st);
 }
 
-static Tile grad_tile(const prism_linear_t &l) {
-  return choose(kGradTiles, 2, l.out, l.in, (int)((l.n + gemm::BK - 1) / gemm::BK), true);
+static Plan grad_plan(const prism_linear_t &l) {
+  // the same plan for both output types, so that a workspace fits either
+  return make_plan(l.out, l.in, (int)((l.n + gemm::BK - 1) / gemm::BK), true, gemm::kChain, false);
 }
-static Sched grad_sched(const prism_linear_t &l, const Tile &t) {
-  return make_sched(t, l.out, l.in, (int)((l.n + gemm::BK - 1) / gemm::BK), true);
+static size_t grad_part_bytes(const Plan &p) {
+  return p.s.rem ? sizeof(float) * (size_t)(p.s.groups + p.s.rem) * (128 * p.cg) * p.bn : 0;
 }
-static size_t grad_part_bytes(const prism_linear_t &l) {
-  const Tile t = grad_tile(l);
-  const Sched s = grad_sched(l, t);
-  return s.rem ? sizeof(float) * (size_t)(s.groups + s.rem) * (128 * t.cg) * t.bn : 0;
-}
+// A checkpointed X is converted on its way to the tensor cores, once for every
+// 256 output channels.  From 2048 of them on, restoring it once is faster, and
+// so it is for the small tiles, whose kernels read bf16 only.  Measured at
+// 92160 x 1024: out = 1024, 185 us against 53 + 155; out = 4096, 703 against
+// 53 + 553.
+static bool grad_restores(const prism_linear_t &l, const Plan &p) { return p.split || p.cg == 1 || l.out >= 2048; }
 
 // dW [out][in] = dZ^T X, summed over the tokens
 static cudaError_t weight_grad(const prism_linear_t &l, const uint16_t *dZ, long long ldd, const uint16_t *X,
-                               long long ldx, const prism_ckpt8_t *X8, void *dW, int fp32, float *part, int *status,
-                               cudaStream_t st) {
-  const Tile t = grad_tile(l);
+                               long long ldx, const prism_ckpt8_t *X8, uint16_t *restored, void *dW, int fp32,
+                               float *part, int *status, int reset, cudaStream_t st) {
+  const Plan p = grad_plan(l);
+  cudaError_t e;
+  if (X8 && grad_restores(l, p)) {
+    if ((e = launch_ckpt8_unpack(*X8, l.n, l.in, restored, l.in, st)) != cudaSuccess) return e;
+    X = restored;
+    ldx = l.in;
+    X8 = nullptr;
+  }
   Args a = {};
-  a.s = grad_sched(l, t);
+  a.s = p.s;
   a.rows = l.out;
   a.cols = l.in;
   a.status = status;
-  const int bm = 128 * t.cg;
+  a.reset = reset;
+  const int bm = 128 * p.cg;
   Maps m;
-  cudaError_t e;
   if ((e = rows_map(&m.a, dZ, l.out, l.n, ldd, gemm::BK)) != cudaSuccess) return e;
   if (X8)
     e = make_map_2d(&m.b, MAP_U8, X8->codes, l.in, l.n, X8->ld, 128, gemm::BK);
   else
     e = rows_map(&m.b, X, l.in, l.n, ldx, gemm::BK);
   if (e != cudaSuccess) return e;
+  if (p.split) {
+    a.Y = dW;
+    a.ldy = l.in;
+    a.out_fp32 = fp32;
+    return launch_split<true, true>(p, m, a, st);
+  }
   if (fp32)
     e = make_map_2d(&m.y, MAP_F32, dW, l.in, l.out, l.in, 32, 32);
   else
     e = rows_map(&m.y, dW, l.in, l.out, l.in, 32);
   if (e != cudaSuccess) return e;
   m.r = m.z = m.y;
-  if (a.s.rem &&
-      (e = make_map_2d(&m.z, MAP_F32, part, t.bn, (long long)(a.s.groups + a.s.rem) * bm, t.bn, 32, 32)) != cudaSuccess)
+  if (p.s.rem &&
+      (e = make_map_2d(&m.z, MAP_F32, part, p.bn, (long long)(p.s.groups + p.s.rem) * bm, p.bn, 32, 32)) != cudaSuccess)
     return e;
   if (X8) {
     a.b_scales = X8->scales;
     a.b_ld = X8->ld;
     a.k_total = (int)l.n;
-    e = fp32 ? launch_grad<true, true>(t, m, a, st) : launch_grad<true, false>(t, m, a, st);
+    e = fp32 ? launch<Cfg<2, 256, true, true, true, true>>(m, a, st) : launch<Cfg<2, 256, true, true, true, false>>(m, a, st);
+  } else if (p.cg == 2) {
+    e = fp32 ? launch<Cfg<2, 256, true, true, false, true>>(m, a, st)
+             : launch<Cfg<2, 256, true, true, false, false>>(m, a, st);
   } else {
-    e = fp32 ? launch_grad<false, true>(t, m, a, st) : launch_grad<false, false>(t, m, a, st);
+    e = fp32 ? launch<Cfg<1, 128, true, true, false, true>>(m, a, st)
+             : launch<Cfg<1, 128, true, true, false, false>>(m, a, st);
   }
-  if (e != cudaSuccess || !a.s.rem) return e;
-  sum_parts_kernel<<<dim3(bm * t.bn / 1024, a.s.rem), 256, 0, st>>>(part, a.s, bm, t.bn, l.out, l.in, dW, fp32);
+  if (e != cudaSuccess || !p.s.rem) return e;
+  // rows of threads by the parts of a tile
+  const int parts = p.s.groups / p.s.rem + 2, outputs = bm * p.bn;
+  if (parts <= 8)
+    sum_parts_kernel<1><<<dim3(outputs / 4096, p.s.rem), 256, 0, st>>>(part, p.s, bm, p.bn, l.out, l.in, dW, fp32);
+  else
+    sum_parts_kernel<8><<<dim3(outputs / 512, p.s.rem), 256, 0, st>>>(part, p.s, bm, p.bn, l.out, l.in, dW, fp32);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -309,14 +419,14 @@ static int check_workspace(void *ws, size_t bytes, size_t need) {
 }
 
 // workspace of the backward: header, dZ (with an activation), the bias
-// gradient's partial sums, the weight gradient's
+// gradient's partial sums, the weight gradient's, X where it is restored
 struct BwdWs {
-  uint16_t *dZ;
+  uint16_t *dZ, *X;
   float *bias_part, *part;
   size_t bytes;
 };
-static BwdWs carve_bwd(const prism_linear_t &l, void *ws) {
-  BwdWs b;
+static BwdWs carve_bwd(const prism_linear_t &l, bool x8, void *ws) {
+  BwdWs b = {};
   size_t at = kWsHeader;
   char *w = static_cast<char *>(ws);
   b.dZ = reinterpret_cast<uint16_t *>(w + at);
@@ -324,7 +434,12 @@ static BwdWs carve_bwd(const prism_linear_t &l, void *ws) {
   b.bias_part = reinterpret_cast<float *>(w + at);
   at += act_grad_part_bytes(l.n, l.out);
   b.part = reinterpret_cast<float *>(w + at);
-  at += grad_part_bytes(l);
+  if (l.n > 0) {
+    const Plan p = grad_plan(l);
+    at += grad_part_bytes(p);
+    b.X = reinterpret_cast<uint16_t *>(w + at);
+    if (x8 && grad_restores(l, p)) at += align_up(2 * (size_t)l.n * l.in, 256);
+  }
   b.bytes = at;
   return b;
 }
@@ -339,7 +454,8 @@ extern "C" {
 
 size_t prism_linear_workspace_size(const prism_linear_t *l, int backward) {
   if (check_linear(l) != PRISM_OK) return 0;
-  return backward ? carve_bwd(*l, nullptr).bytes : kWsHeader;
+  if (backward < 0 || backward > 2) return 0;
+  return backward ? carve_bwd(*l, backward == 2, nullptr).bytes : kWsHeader;
 }
 
 int prism_linear_fwd(const prism_linear_t *l, const uint16_t *X, int64_t ldx, const uint16_t *W, const uint16_t *bias,
@@ -358,8 +474,10 @@ int prism_linear_fwd(const prism_linear_t *l, const uint16_t *X, int64_t ldx, co
   if (Z8 && l->n > 0 && (rc = check_ckpt("Z8", Z8, l->out)) != PRISM_OK) return rc;
   if ((rc = check_workspace(workspace, ws_bytes, kWsHeader)) != PRISM_OK) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(workspace, 0, kWsHeader, st);
-  if (e == cudaSuccess && l->n > 0)
+  cudaError_t e;
+  if (l->n == 0)
+    e = cudaMemsetAsync(workspace, 0, kWsHeader, st);
+  else
     e = forward(*l, X, ldx, W, bias, R, ldr, Y, ldy, Z, Z8, &static_cast<WsHeader *>(workspace)->status, st);
   if (e != cudaSuccess) return refuse(PRISM_ERR_CUDA, "prism_linear_fwd: %s", cudaGetErrorString(e));
   clear_error();
@@ -390,22 +508,24 @@ int prism_linear_bwd(const prism_linear_t *l, const uint16_t *dY, int64_t lddy, 
   if ((rc = check_rows("W", W, l->in, l->in)) != PRISM_OK || (rc = check_rows("dX", dX, l->in, l->in)) != PRISM_OK ||
       (rc = check_rows("dW", dW, l->in, l->in)) != PRISM_OK || (rc = check_rows("db", db, l->out, l->out)) != PRISM_OK)
     return rc;
-  const BwdWs b = carve_bwd(*l, workspace);
+  const BwdWs b = carve_bwd(*l, X8 != nullptr, workspace);
   if ((rc = check_workspace(workspace, ws_bytes, b.bytes)) != PRISM_OK) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(workspace, 0, kWsHeader, st);
+  cudaError_t e = cudaSuccess;
   const size_t elem = grad_fp32 ? 4 : 2;
   if (l->n == 0) {  // empty sums
+    e = cudaMemsetAsync(workspace, 0, kWsHeader, st);
     if (e == cudaSuccess && dW) e = cudaMemsetAsync(dW, 0, elem * l->in * l->out, st);
     if (e == cudaSuccess && db) e = cudaMemsetAsync(db, 0, elem * l->out, st);
   } else {
     int *status = &static_cast<WsHeader *>(workspace)->status;
     const uint16_t *dZ = act ? b.dZ : dY;
     const long long ldd = act ? l->out : lddy;
-    if (e == cudaSuccess && (act || db))
-      e = launch_act_grad(l->n, l->out, l->act, dY, lddy, Z, ldz, Z8, b.dZ, b.bias_part, db, grad_fp32, st);
-    if (e == cudaSuccess && dX) e = input_grad(*l, dZ, ldd, W, dX, status, st);
-    if (e == cudaSuccess && dW) e = weight_grad(*l, dZ, ldd, X, ldx, X8, dW, grad_fp32, b.part, status, st);
+    const bool first = act || db;
+    if (first) e = launch_act_grad(l->n, l->out, l->act, dY, lddy, Z, ldz, Z8, b.dZ, b.bias_part, db, grad_fp32, status, st);
+    if (e == cudaSuccess && dX) e = input_grad(*l, dZ, ldd, W, dX, status, !first, st);
+    if (e == cudaSuccess && dW)
+      e = weight_grad(*l, dZ, ldd, X, ldx, X8, b.X, dW, grad_fp32, b.part, status, !first && !dX, st);
   }
   if (e != cudaSuccess) return refuse(PRISM_ERR_CUDA, "prism_linear_bwd: %s", cudaGetErrorString(e));
   clear_error();

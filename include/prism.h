@@ -423,9 +423,9 @@ typedef struct prism_linear_t {
   int32_t act;
 } prism_linear_t;
 
-/* Bytes of workspace prism_linear_fwd (backward = 0) or prism_linear_bwd
- * (backward = 1: any choice of gradients, bf16 or checkpointed inputs) needs on
- * the current device (0 on an invalid description). */
+/* Bytes of workspace prism_linear_fwd (backward = 0) or prism_linear_bwd needs
+ * (backward = 1 with X in bf16, 2 with X as a checkpoint; for any choice of
+ * gradients) on the current device (0 on an invalid description). */
 size_t prism_linear_workspace_size(const prism_linear_t *l, int backward);
 
 /*
@@ -460,8 +460,8 @@ int prism_linear_fwd(const prism_linear_t *l, const uint16_t *X, int64_t ldx,
  * (The gradient of R is dY.)
  *   dY      bf16 [n][lddy].
  *   X, X8   the forward's input: bf16 [n][ldx], or its checkpoint (the other
- *           NULL).  Needed for dW.  The products read the checkpoint's codes;
- *           X is not restored in memory.
+ *           NULL).  Needed for dW.  The checkpoint's values are exact in bf16:
+ *           dW is what the restored X would give.
  *   W       bf16 [out][in].  Needed for dX.
  *   Z, Z8   the forward's pre-activation, bf16 [n][ldz] or a checkpoint (the
  *           other NULL).  Needed unless act is PRISM_ACT_NONE (then ignored).

@@ -314,8 +314,10 @@ def test_offsets_past_32_bits():
     assert torch.equal(f.Y[pick], part.Y)
     assert torch.equal(f.Z.codes[pick], part.Z.codes) and torch.equal(f.Z.scales[pick], part.Z.scales)
     g = api.linear_bwd(f.Y, d["X"], d["W"], need=("dX",))
-    gp = api.linear_bwd(part.Y, d["X"][pick].contiguous(), d["W"], need=("dX",))
-    assert torch.equal(g.dX[pick], gp.dX)
+    dY, W = _np(part.Y), _np(d["W"])
+    want, mag = dY @ W, np.abs(dY) @ np.abs(W)
+    tol = cout * STEP * mag
+    _within(g.dX[pick], want, tol + 2.0 ** -8 * (np.abs(want) + tol), "dX")
 
 
 def test_layer_training_step_through_checkpoints():

@@ -41,7 +41,7 @@ def test_struct_layouts():
                                 dict(act=4), dict(act=-1)])
 def test_bad_descriptions(kw):
     lib = _lib.load()
-    for backward in (0, 1):
+    for backward in (0, 1, 2):
         assert lib.prism_linear_workspace_size(_lin(**kw), backward) == 0
     assert _fwd(_lin(**kw)) == BAD and _bwd(_lin(**kw)) == BAD
     assert "linear" in lib.prism_last_error().decode()
@@ -75,6 +75,10 @@ def test_workspaces():
     act = lib.prism_linear_workspace_size(_lin(n=4096, i=512, o=256, act=3), 1)
     assert act - plain == 2 * 4096 * 256          # dZ
     assert _bwd(_lin(n=4096, i=512, o=256), lddy=256, ldx=512, size=plain - 1) == _lib.PRISM_ERR_CAPACITY
+    x8 = lib.prism_linear_workspace_size(_lin(n=4096, i=512, o=2048), 2)
+    assert x8 >= lib.prism_linear_workspace_size(_lin(n=4096, i=512, o=2048), 1) + 2 * 4096 * 512   # X restored
+    assert lib.prism_linear_workspace_size(_lin(), 3) == 0
+    assert api.linear_workspace_size(4096, 512, 2048, backward=True, x8=True) == x8
     assert api.linear_workspace_size(4096, 512, 256, api.ACT_GELU, True) == act
     with pytest.raises(_lib.PrismError):
         api.linear_workspace_size(4096, 12, 256)
