@@ -402,7 +402,8 @@ __device__ __forceinline__ void stage_fp32(const CUtensorMap *map, uint8_t *buf,
 // bf16, 128-byte swizzled as the tensor maps are), one for each of the at most
 // two 64-column chunks it owns: a buffer receives its chunk's residual by TMA
 // while the products run, then the result, then feeds the TMA store.  When the
-// pre-activation is saved in bf16, it takes the second buffer.
+// pre-activation is saved, it takes the second buffer: in bf16 chunk by chunk, as
+// codes (128 bytes a row) for both chunks at once.
 template <class C>
 __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUtensorMap &mapR, const CUtensorMap &mapZ,
                                               const Args &args, Bars &bar, uint8_t *staging, uint32_t tmem, int group,
@@ -419,6 +420,9 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
   const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
   const int sw = lane & 7;
   const bool z16 = args.save_z == 1;
+  // codes through the second staging buffer; a single chunk's 64 bytes a row go straight to memory
+  const bool z8 = PER == 2 && C::NBUF == 2 && args.save_z == 2;
+  const bool solo = z16 || z8;  // the result has one buffer
   SegIter it(s, group);
   Seg sg;
   int t = 0;
@@ -443,12 +447,13 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
     if (args.has_res) {
       if (lane == 0) store_wait_read<0>();
       __syncwarp();
-      for (int c = 0; c < (z16 ? min(n_ch, 1) : n_ch); ++c) load_res(c, c);
+      for (int c = 0; c < (solo ? min(n_ch, 1) : n_ch); ++c) load_res(c, c);
     }
     ok = __all_sync(0xffffffffu, mbar_wait(&bar.acc_full[ab], (t >> 1) & 1, status, 407));
     if (ok) {
       tc_fence_after();
       const uint32_t acc = tmem + ab * C::BN + c_lo * 64 + lane_off;
+      uint32_t scale4 = 0;
       if (parts) {
         if (lane == 0) store_wait_read<0>();
         __syncwarp();
@@ -467,24 +472,24 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
       for (int c = 0; c < (parts ? 0 : n_ch); ++c) {
         const int col0 = n0 + c * 64;
         const bool in = rows_in && col0 < args.cols;
-        const int yb = z16 || C::NBUF == 1 ? 0 : c;
-        if (z16 && c > 0) {
+        const int yb = solo || C::NBUF == 1 ? 0 : c;
+        if (solo && c > 0) {
           if (lane == 0) store_wait_read<0>();
           __syncwarp();
           load_res(c, 0);
         }
         const bool res = (res_pending >> yb) & 1;
         if (!args.has_res) {
-          // this buffer's last store was the one before the last (z16: the last)
+          // this buffer's last store was the one before the last (solo: the last)
           if (lane == 0) {
-            if (z16 || C::BN < 256 || C::NBUF == 1)
+            if (solo || C::BN < 256 || C::NBUF == 1)
               store_wait_read<0>();
             else
               store_wait_read<1>();
           }
           __syncwarp();
         }
-        uint32_t scale2 = 0;
+        if (!z8 || c == 0) scale4 = 0;
         uint8_t *row = buf + yb * kStageBuf + lane * 128;
 #pragma unroll 1
         for (int g = 0; g < 2; ++g) {
@@ -500,8 +505,15 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4 *>(row + kStageBuf + (((g * 4 + i) ^ sw) << 4)) = pack8(v, 4 * i);
+          } else if (z8) {
+            uint32_t q[8];
+            scale4 |= ckpt8_quantise(v, q) << (8 * (2 * c + g));
+            uint8_t *qrow = buf + kStageBuf + lane * 128;
+            const int u0 = 4 * c + 2 * g;
+            *reinterpret_cast<uint4 *>(qrow + ((u0 ^ sw) << 4)) = make_uint4(q[0], q[1], q[2], q[3]);
+            *reinterpret_cast<uint4 *>(qrow + (((u0 + 1) ^ sw) << 4)) = make_uint4(q[4], q[5], q[6], q[7]);
           } else if (args.save_z == 2) {
-            scale2 |= save_codes(v, args, m0 + lane, cg0) << (8 * g);
+            scale4 |= save_codes(v, args, m0 + lane, cg0) << (8 * g);
           }
           apply_act(v, args.act);
           if (res && g == 0) {
@@ -523,9 +535,13 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
           }
         }
         if (!ok) break;
-        if (args.save_z == 2 && m0 + lane < args.rows && col0 < args.ldq)
-          *reinterpret_cast<uint16_t *>(args.scales + (long long)(m0 + lane) * (args.ldq / 32) + col0 / 32) =
-              (uint16_t)scale2;
+        if (args.save_z == 2 && m0 + lane < args.rows && col0 < args.ldq) {
+          uint8_t *sp = args.scales + (long long)(m0 + lane) * (args.ldq / 32) + col0 / 32;
+          if (!z8)
+            *reinterpret_cast<uint16_t *>(sp) = (uint16_t)scale4;
+          else if (c == 1)
+            *reinterpret_cast<uint32_t *>(sp - 2) = scale4;
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -533,6 +549,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
             store_2d(&mapY, buf + yb * kStageBuf, col0, m0);
             if (z16) store_2d(&mapZ, buf + kStageBuf, col0, m0);
           }
+          if (z8 && c == 1 && rows_in && n0 < args.ldq) store_2d(&mapZ, buf + kStageBuf, n0, m0);
           store_commit();
         }
       }

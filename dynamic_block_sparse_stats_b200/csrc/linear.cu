@@ -263,6 +263,7 @@ static cudaError_t forward(const prism_linear_t &l, const uint16_t *X, long long
     m.r = m.z = m.y;
     if (R && (e = rows_map(&m.r, R, cols, rows, ldr, 32)) != cudaSuccess) return e;
     if (Z && (e = rows_map(&m.z, Z, cols, rows, cols, 32)) != cudaSuccess) return e;
+    if (Z8 && (e = make_map_2d(&m.z, MAP_U8_SW, Z8->codes, Z8->ld, rows, Z8->ld, 128, 32)) != cudaSuccess) return e;
   }
   return launch_plan<false, false>(p, m, a, st);
 }
