@@ -340,17 +340,16 @@ __device__ __forceinline__ uint4 pack8(const float2 (&v)[16], int i) {
                     pack_bf16(v[i + 3].x, v[i + 3].y));
 }
 
-// 32 columns of a row, from column c0
-__device__ __forceinline__ void add_bias(float2 (&v)[16], const uint16_t *bias, int c0, int cols) {
+// The bias of a warp's (at most 128) columns, four to a lane, loaded while the
+// products still run; add_bias hands a group of 32 columns round by shuffles.
+__device__ __forceinline__ uint2 load_bias(const uint16_t *bias, int c0, int lane, int cols) {
+  const int c = c0 + lane * 4;
+  return bias && c < cols ? __ldg(reinterpret_cast<const uint2 *>(bias + c)) : make_uint2(0, 0);
+}
+__device__ __forceinline__ void add_bias(float2 (&v)[16], const uint2 &b, int group) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (c0 + i * 8 < cols) {
-      const uint4 b = __ldg(reinterpret_cast<const uint4 *>(bias + c0) + i);
-      const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[4 * i + k] = fadd2(v[4 * i + k], bf16_pair(w[k]));
-    }
-  }
+  for (int p = 0; p < 16; ++p)
+    v[p] = fadd2(v[p], bf16_pair(__shfl_sync(0xffffffffu, p & 1 ? b.y : b.x, group * 8 + (p >> 1))));
 }
 __device__ __forceinline__ void apply_act(float2 (&v)[16], int act) {
   switch (act) {
@@ -449,6 +448,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
       __syncwarp();
       for (int c = 0; c < (solo ? min(n_ch, 1) : n_ch); ++c) load_res(c, c);
     }
+    const uint2 bias = load_bias(args.bias, n0, lane, min(args.cols, n0 + n_ch * 64));
     ok = __all_sync(0xffffffffu, mbar_wait(&bar.acc_full[ab], (t >> 1) & 1, status, 407));
     if (ok) {
       tc_fence_after();
@@ -500,7 +500,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
           float2 v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-          if (args.bias) add_bias(v, args.bias, cg0, args.cols);
+          if (args.bias) add_bias(v, bias, 2 * c + g);
           if (z16) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)

@@ -36,8 +36,11 @@ using gemm::Sched;
 //           bound, 80% of the tensor pipe), 6.0 around them
 //   single  128 x 128 tiles, persistent: 0.35 a stage (L2 bound), 4.2 around
 //   split   128 x 64 tiles, the contraction over up to 8 CTAs of a cluster: 0.33
-//           a stage, 5.0 around, one tile per cluster
-// The least estimate is taken.
+//           a stage, 5.0 (8 CTAs) to 8.1 (one) around, one tile per cluster
+// An epilogue with an activation, a residual or a saved Z adds 4.0, 1.8 and 0.3
+// behind the last tile.  The least estimate is taken; against all three timed at
+// 27 sizes from 1 x 1024 x 4096 to 92160 x 1024 x 1024, the choice is within a tenth
+// of the best.
 struct Plan {
   int cg, bn;  // tile: 128 * cg rows, bn columns
   int split;   // > 0: split_kernel with clusters of this size
@@ -46,6 +49,7 @@ struct Plan {
   double us;
 };
 constexpr int kMaxSplit = 8;
+constexpr int kMaxGroups = 160;
 
 static Sched make_sched(int cg, int bn, int rows, int cols, int kc, bool share) {
   Sched s;
@@ -56,7 +60,7 @@ static Sched make_sched(int cg, int bn, int rows, int cols, int kc, bool share) 
   s.full = s.tiles;
   s.rem = 0;
   s.km = kc;
-  const int most = device_sm_count() / cg;
+  const int most = std::min(device_sm_count() / cg, kMaxGroups);
   s.groups = std::min(most, s.tiles);
   if (share) {
     // at least 8 stages a group: below that the partial sums cost more than the products
@@ -78,7 +82,7 @@ static Sched make_sched(int cg, int bn, int rows, int cols, int kc, bool share) 
 
 // share: the tiles of the last wave may be divided (the weight gradient's);
 // chain: longest part of the contraction the split kernel may take in one sum
-static Plan make_plan(int rows, int cols, int kc, bool share, int chain, bool may_swap) {
+static Plan make_plan(int rows, int cols, int kc, bool share, int chain, bool may_swap, bool heavy) {
   Plan best = {};
   best.us = 1e300;
   const int sms = device_sm_count();
@@ -88,8 +92,9 @@ static Plan make_plan(int rows, int cols, int kc, bool share, int chain, bool ma
     p.bn = big ? 256 : 128;
     p.s = make_sched(p.cg, p.bn, rows, cols, kc, share);
     const double waves = p.s.rem ? (double)p.s.full / p.s.groups : (double)((p.s.tiles + p.s.groups - 1) / p.s.groups);
-    p.us = (big ? 6.0 : 4.2) + waves * kc * (big ? 0.40 : 0.35);
-    if (p.s.rem) p.us += p.s.km * (big ? 0.40 : 0.35) + 5.0;  // and the kernel that adds the parts
+    p.us = (big ? 6.0 : 4.2) + (heavy ? (big ? 4.0 : 1.8) : 0.0) + waves * kc * (big ? 0.40 : 0.35);
+    // the shared tiles, and the kernel that adds their parts
+    if (p.s.rem) p.us += p.s.km * (big ? 0.40 : 0.35) + 5.0 + 0.02 * p.s.groups / p.s.rem;
     if (p.us < best.us) best = p;
   }
   Plan p = {};
@@ -101,7 +106,7 @@ static Plan make_plan(int rows, int cols, int kc, bool share, int chain, bool ma
     p.split = 1;
     while (p.split < kMaxSplit && 2 * p.split * p.s.tiles <= sms && 2 * p.split <= kc) p.split *= 2;
     const int part = (kc + p.split - 1) / p.split;
-    p.us = 5.0 + part * 0.33;
+    p.us = 4.5 + 3.6 / p.split + (heavy ? 0.3 : 0.0) + part * 0.33;
     if (part <= chain && p.us < best.us) best = p;
   }
   return best;
@@ -113,10 +118,15 @@ static Plan make_plan(int rows, int cols, int kc, bool share, int chain, bool ma
 // dW of the split tiles = their slots in a fixed order: the first part, then the
 // helpers' parts.  Y rows of threads take every Y-th part each and meet in shared
 // memory, so that a small output cut into many parts (64 x 64 over 92160 tokens:
-// 149) is read by enough threads; a CTA owns 4096 / Y outputs.
-template <int Y>
+// 149) is read by enough threads; a CTA owns 1024 ITER / Y outputs.
+// The helpers [first, last) of each split tile come with the launch: finding them
+// takes 64-bit divisions, which cost more than the sums.
+struct Helpers {
+  uint8_t first[kMaxGroups], last[kMaxGroups];
+};
+template <int Y, int ITER>
 __global__ void __launch_bounds__(256)
-    sum_parts_kernel(const float *__restrict__ part, const Sched s, int bm, int bn, int rows, int cols,
+    sum_parts_kernel(const float *__restrict__ part, const Sched s, const Helpers who, int bm, int bn, int rows, int cols,
                      void *__restrict__ out, int fp32) {
   constexpr int LANES = 256 / Y;
   __shared__ float4 red[Y > 1 ? Y : 1][LANES];
@@ -124,18 +134,12 @@ __global__ void __launch_bounds__(256)
   const int tile = s.full + t;
   const int row0 = (tile / s.tiles_n) * bm, col0 = (tile % s.tiles_n) * bn;
   const long long slot = (long long)bm * bn;
-  const long long lo = (long long)t * (s.kc - s.km), hi = lo + (s.kc - s.km);
-  const int helpers = s.groups - s.rem;
-  // the helpers [h0, h1) whose ranges meet tile t's tail: starts are rem * tail * h / helpers, rounded down
-  int h0 = max(0, (int)((long long)t * helpers / s.rem) - 1);
-  while (gemm::helper_start(s, h0 + 1) <= lo) ++h0;
-  int h1 = h0 + 1;
-  while (h1 < helpers && gemm::helper_start(s, h1) < hi) ++h1;
+  const int h0 = who.first[t], h1 = who.last[t];
   const float *first = part + t * slot, *more = part + (s.rem + h0 + t) * slot;
   const int parts = 1 + h1 - h0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = ((blockIdx.x * 4 + i) * LANES + lane) * 4;
+  for (int i = 0; i < ITER; ++i) {
+    const int e = ((blockIdx.x * ITER + i) * LANES + lane) * 4;
     const int row = row0 + e / bn, col = col0 + e % bn;
     const bool in = row < rows && col < cols;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -223,15 +227,12 @@ static cudaError_t launch_plan(const Plan &p, const Maps &m, const Args &args, c
   return launch<Cfg<1, 128, A_MN, B_MN>>(m, args, st);
 }
 
-static Plan forward_plan(const prism_linear_t &l) {
-  return make_plan((int)l.n, l.out, (l.in + gemm::BK - 1) / gemm::BK, false, 1 << 30, true);
-}
-
 static cudaError_t forward(const prism_linear_t &l, const uint16_t *X, long long ldx, const uint16_t *W,
                            const uint16_t *bias, const uint16_t *R, long long ldr, uint16_t *Y, long long ldy,
                            uint16_t *Z, const prism_ckpt8_t *Z8, int *status, cudaStream_t st) {
   const int rows = (int)l.n, cols = l.out;
-  const Plan p = forward_plan(l);
+  const Plan p = make_plan(rows, cols, (l.in + gemm::BK - 1) / gemm::BK, false, 1 << 30, true,
+                           l.act != PRISM_ACT_NONE || R || Z || Z8);
   Maps m;
   cudaError_t e;
   CUtensorMap &mx = p.swap ? m.b : m.a, &mw = p.swap ? m.a : m.b;
@@ -272,7 +273,7 @@ static cudaError_t forward(const prism_linear_t &l, const uint16_t *X, long long
 static cudaError_t input_grad(const prism_linear_t &l, const uint16_t *dZ, long long ldd, const uint16_t *W,
                               uint16_t *dX, int *status, int reset, cudaStream_t st) {
   const int rows = (int)l.n, cols = l.in;
-  const Plan p = make_plan(rows, cols, (l.out + gemm::BK - 1) / gemm::BK, false, 1 << 30, true);
+  const Plan p = make_plan(rows, cols, (l.out + gemm::BK - 1) / gemm::BK, false, 1 << 30, true, false);
   Maps m;
   cudaError_t e;
   CUtensorMap &mz = p.swap ? m.b : m.a, &mw = p.swap ? m.a : m.b;
@@ -294,9 +295,8 @@ static cudaError_t input_grad(const prism_linear_t &l, const uint16_t *dZ, long 
   return launch_plan<false, true>(p, m, a, st);
 }
 
-static Plan grad_plan(const prism_linear_t &l) {
-  // the same plan for both output types, so that a workspace fits either
-  return make_plan(l.out, l.in, (int)((l.n + gemm::BK - 1) / gemm::BK), true, gemm::kChain, false);
+static Plan grad_plan(const prism_linear_t &l, bool fp32) {
+  return make_plan(l.out, l.in, (int)((l.n + gemm::BK - 1) / gemm::BK), true, fp32 ? gemm::kChain : 1 << 30, false, false);
 }
 static size_t grad_part_bytes(const Plan &p) {
   return p.s.rem ? sizeof(float) * (size_t)(p.s.groups + p.s.rem) * (128 * p.cg) * p.bn : 0;
@@ -312,7 +312,7 @@ static bool grad_restores(const prism_linear_t &l, const Plan &p) { return p.spl
 static cudaError_t weight_grad(const prism_linear_t &l, const uint16_t *dZ, long long ldd, const uint16_t *X,
                                long long ldx, const prism_ckpt8_t *X8, uint16_t *restored, void *dW, int fp32,
                                float *part, int *status, int reset, cudaStream_t st) {
-  const Plan p = grad_plan(l);
+  const Plan p = grad_plan(l, fp32);
   cudaError_t e;
   if (X8 && grad_restores(l, p)) {
     if ((e = launch_ckpt8_unpack(*X8, l.n, l.in, restored, l.in, st)) != cudaSuccess) return e;
@@ -362,12 +362,22 @@ static cudaError_t weight_grad(const prism_linear_t &l, const uint16_t *dZ, long
              : launch<Cfg<1, 128, true, true, false, false>>(m, a, st);
   }
   if (e != cudaSuccess || !p.s.rem) return e;
+  Helpers who = {};
+  const long long tail = p.s.kc - p.s.km;
+  for (int t = 0, h = 0; t < p.s.rem; ++t) {
+    // shares are at least one stage, so that a tail's helpers follow one another
+    while (gemm::helper_start(p.s, h + 1) <= t * tail) ++h;
+    who.first[t] = (uint8_t)h;
+    int last = h + 1;
+    while (last < p.s.groups - p.s.rem && gemm::helper_start(p.s, last) < (t + 1) * tail) ++last;
+    who.last[t] = (uint8_t)last;
+  }
   // rows of threads by the parts of a tile
   const int parts = p.s.groups / p.s.rem + 2, outputs = bm * p.bn;
   if (parts <= 8)
-    sum_parts_kernel<1><<<dim3(outputs / 4096, p.s.rem), 256, 0, st>>>(part, p.s, bm, p.bn, l.out, l.in, dW, fp32);
+    sum_parts_kernel<1, 4><<<dim3(outputs / 4096, p.s.rem), 256, 0, st>>>(part, p.s, who, bm, p.bn, l.out, l.in, dW, fp32);
   else
-    sum_parts_kernel<8><<<dim3(outputs / 512, p.s.rem), 256, 0, st>>>(part, p.s, bm, p.bn, l.out, l.in, dW, fp32);
+    sum_parts_kernel<8, 1><<<dim3(outputs / 128, p.s.rem), 256, 0, st>>>(part, p.s, who, bm, p.bn, l.out, l.in, dW, fp32);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -391,6 +401,8 @@ static int check_linear(const prism_linear_t *l) {
   if (l->in <= 0 || l->in % 8 || l->in > (1 << 16) || l->out <= 0 || l->out % 8 || l->out > (1 << 16))
     return refuse(PRISM_ERR_INVALID_ARG, "linear: in and out must be positive multiples of 8, at most 65536 (got %d, %d)",
                   l->in, l->out);
+  if (l->n * std::max(l->in, l->out) >= (1LL << 40))
+    return refuse(PRISM_ERR_UNSUPPORTED, "linear: more than 2^40 values (n = %lld)", (long long)l->n);
   if (l->act < PRISM_ACT_NONE || l->act > PRISM_ACT_GELU)
     return refuse(PRISM_ERR_INVALID_ARG, "linear: act must be 0..3 (got %d)", l->act);
   return PRISM_OK;
@@ -436,10 +448,10 @@ static BwdWs carve_bwd(const prism_linear_t &l, bool x8, void *ws) {
   at += act_grad_part_bytes(l.n, l.out);
   b.part = reinterpret_cast<float *>(w + at);
   if (l.n > 0) {
-    const Plan p = grad_plan(l);
-    at += grad_part_bytes(p);
+    const Plan p = grad_plan(l, false), q = grad_plan(l, true);  // room for either output type
+    at += std::max(grad_part_bytes(p), grad_part_bytes(q));
     b.X = reinterpret_cast<uint16_t *>(w + at);
-    if (x8 && grad_restores(l, p)) at += align_up(2 * (size_t)l.n * l.in, 256);
+    if (x8 && (grad_restores(l, p) || grad_restores(l, q))) at += align_up(2 * (size_t)l.n * l.in, 256);
   }
   b.bytes = at;
   return b;

@@ -410,7 +410,7 @@ int prism_ckpt8_unpack(const prism_ckpt8_t *in, int64_t n, int32_t width,
 
 /*
  * A linear map of n tokens from `in` to `out` channels with an activation.
- *   n        tokens, 0 <= n < 2^30.
+ *   n        tokens, 0 <= n < 2^30, with n * in and n * out below 2^40.
  *   in, out  channels, positive multiples of 8, at most 65536.
  *   act      PRISM_ACT_NONE, PRISM_ACT_RELU, PRISM_ACT_SILU, or
  *            PRISM_ACT_GELU (tanh form:
