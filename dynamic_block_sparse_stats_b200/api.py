@@ -612,66 +612,72 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
     is dY itself."""
     lddy = _check_rows(dY, "dY")
     n, cout = dY.shape
-    need = tuple(need)
-    if not need or any(k not in ("dX", "dW", "db") for k in need):
+    if not need or not all(k in ("dX", "dW", "db") for k in need):
         raise ValueError(f'need must name some of "dX", "dW", "db", got {need!r}')
-    if "dX" in need and W is None:
+    want_x, want_w, want_b = "dX" in need, "dW" in need, "db" in need
+    if want_x and W is None:
         raise ValueError("dX needs W")
-    if "dW" in need and X is None:
+    if want_w and X is None:
         raise ValueError("dW needs X")
+    x8 = isinstance(X, Ckpt8)
     if W is not None:
         if not isinstance(W, torch.Tensor) or W.dim() != 2:
             raise ValueError("W must be a 2-D tensor [out, in]")
         cin = W.shape[1]
         _check_tensor(W, "W", torch.bfloat16, (cout, cin))
     elif X is not None:
-        cin = X.width if isinstance(X, Ckpt8) else X.shape[-1]
+        cin = X.width if x8 else X.shape[-1]
     else:
         cin = 8  # only db: the input's width does not matter
     named = [("dY", dY), ("W", W)]
     ldx = ldz = 0
-    if isinstance(X, Ckpt8):
+    if x8:
         named += _check_ckpt8(X, "X", n, cin)
     elif X is not None:
         ldx = _check_rows(X, "X", (n, cin))
         named.append(("X", X))
+    z8 = False
     if act == ACT_NONE:
         Z = None
-    elif isinstance(Z, Ckpt8):
-        named += _check_ckpt8(Z, "Z", n, cout)
     elif Z is None:
         raise ValueError("the activation's gradient needs Z")
+    elif isinstance(Z, Ckpt8):
+        z8 = True
+        named += _check_ckpt8(Z, "Z", n, cout)
     else:
         ldz = _check_rows(Z, "Z", (n, cout))
         named.append(("Z", Z))
     dt = torch.float32 if grad_fp32 else torch.bfloat16
-    want = {"dX": ((n, cin), torch.bfloat16), "dW": ((cout, cin), dt), "db": ((cout,), dt)}
-    if out is None:
-        out = (None, None, None)
-    if len(out) != 3:
-        raise ValueError("out must hold three entries (dX, dW, db)")
-    for name, t in zip(("dX", "dW", "db"), out):
-        if t is not None:
-            if name not in need:
-                raise ValueError(f"out holds {name}, which need does not name")
-            _check_tensor(t, name, want[name][1], want[name][0])
-            named.append((name, t))
+    dX = dW = db = None
+    if out is not None:
+        if len(out) != 3:
+            raise ValueError("out must hold three entries (dX, dW, db)")
+        dX, dW, db = out
+        for name, t, wanted, dtype, shape in (("dX", dX, want_x, torch.bfloat16, (n, cin)),
+                                              ("dW", dW, want_w, dt, (cout, cin)), ("db", db, want_b, dt, (cout,))):
+            if t is not None:
+                if not wanted:
+                    raise ValueError(f"out holds {name}, which need does not name")
+                _check_tensor(t, name, dtype, shape)
+                named.append((name, t))
     if ws is not None:
         _check_workspace(ws, "ws")
         named.append(("ws", ws))
     dev = _check_devices(named)
     lib = _lib.load()
     with _on(dev):
-        dX, dW, db = (None if name not in need else
-                      t if t is not None else torch.empty(want[name][0], dtype=want[name][1], device=dev)
-                      for name, t in zip(("dX", "dW", "db"), out))
+        if want_x and dX is None:
+            dX = torch.empty((n, cin), dtype=torch.bfloat16, device=dev)
+        if want_w and dW is None:
+            dW = torch.empty((cout, cin), dtype=dt, device=dev)
+        if want_b and db is None:
+            db = torch.empty((cout,), dtype=dt, device=dev)
         l = PrismLinear(n, cin, cout, act)
-        ws = ws if ws is not None else _workspace(lib.prism_linear_workspace_size(C.byref(l), 2 if isinstance(X, Ckpt8) else 1), dev)
-        x8 = X.c_struct() if isinstance(X, Ckpt8) else None
-        z8 = Z.c_struct() if isinstance(Z, Ckpt8) else None
-        check(lib.prism_linear_bwd(C.byref(l), _addr(dY), lddy, None if x8 is not None else _addr(X), ldx,
-                                   C.byref(x8) if x8 is not None else None, _addr(W),
-                                   None if z8 is not None else _addr(Z), ldz,
-                                   C.byref(z8) if z8 is not None else None, _addr(dX), _addr(dW), _addr(db),
-                                   int(bool(grad_fp32)), _addr(ws), ws.numel(), _handle(stream, dev)))
+        if ws is None:
+            ws = _workspace(lib.prism_linear_workspace_size(C.byref(l), 2 if x8 else 1), dev)
+        cx = C.byref(X.c_struct()) if x8 else None
+        cz = C.byref(Z.c_struct()) if z8 else None
+        check(lib.prism_linear_bwd(C.byref(l), dY.data_ptr(), lddy, None if x8 else _addr(X), ldx, cx, _addr(W),
+                                   None if z8 else _addr(Z), ldz, cz, _addr(dX), _addr(dW), _addr(db),
+                                   1 if grad_fp32 else 0, ws.data_ptr(), ws.numel(), _handle(stream, dev)))
     return LinearGrads(dX, dW, db, ws)

@@ -5,7 +5,7 @@
 // HBM-bound: dY and Z (bf16, or an 8-bit checkpoint) are read once, dZ written
 // once.  A thread owns eight columns (one 16-byte vector) of every k-th row of
 // its block, so its eight fp32 column sums stay in registers; the block's row
-// lanes meet in shared memory, the blocks in a second kernel, all in a fixed
+// lanes meet in shared memory, the blocks in the next launch, all in a fixed
 // order.  Without an activation dZ is dY itself and only the sums are taken.
 #include <algorithm>
 
@@ -141,25 +141,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// db[c] = sum over the blocks: 32 columns per CTA, 8 lanes of blocks each
-__global__ void __launch_bounds__(256)
+// db alone; with a matrix product behind it, that launch's idle warps do this
+__global__ void __launch_bounds__(32)
     bias_grad_kernel(const float *__restrict__ part, int blocks, int cols, void *__restrict__ db, int fp32) {
-  __shared__ float red[8][33];
-  const int cx = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + cx;
-  float a = 0.f;
-  if (c < cols)
-    for (int b = y; b < blocks; b += 8) a += part[(long long)b * cols + c];
-  red[y][cx] = a;
-  __syncthreads();
-  if (y == 0 && c < cols) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) a += red[k][cx];
-    if (fp32)
-      static_cast<float *>(db)[c] = a;
-    else
-      static_cast<uint16_t *>(db)[c] = (uint16_t)(pack_bf16(a, a) & 0xffffu);
-  }
+  gemm::finish_bias(part, blocks, cols, db, fp32, blockIdx.x, gridDim.x, threadIdx.x);
 }
 
 struct Shape {
@@ -205,8 +190,8 @@ size_t act_grad_part_bytes(long long n, int cols) {
 }
 
 cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, long long ldy, const uint16_t *Z,
-                            long long ldz, const prism_ckpt8_t *Z8, uint16_t *dZ, float *part, void *db, int db_fp32,
-                            int *status, cudaStream_t st) {
+                            long long ldz, const prism_ckpt8_t *Z8, uint16_t *dZ, float *part, int *status,
+                            cudaStream_t st) {
   const actg::Shape sh = actg::shape_of(n, cols);
   actg::Src s;
   s.dY = reinterpret_cast<const uint4 *>(dY);
@@ -219,7 +204,7 @@ cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, 
   s.dZ = reinterpret_cast<uint4 *>(dZ);
   s.status = status;
   const dim3 grid(sh.strips, sh.blocks);
-  const actg::Launch l{s, grid, n, cols / 8, sh.tx, sh.rows_per, db ? part : nullptr, st};
+  const actg::Launch l{s, grid, n, cols / 8, sh.tx, sh.rows_per, part, st};
   switch (act) {
     case PRISM_ACT_RELU:
       actg::run<PRISM_ACT_RELU>(l, Z8 != nullptr);
@@ -236,10 +221,15 @@ cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, 
   }
   count_launches(1);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !db) return e;
-  actg::bias_grad_kernel<<<(cols + 31) / 32, 256, 0, st>>>(part, sh.blocks, cols, db, db_fp32);
+  return e;
+}
+
+cudaError_t launch_bias_grad(long long n, int cols, const float *part, void *db, int db_fp32, cudaStream_t st) {
+  actg::bias_grad_kernel<<<(cols + 31) / 32, 32, 0, st>>>(part, actg::shape_of(n, cols).blocks, cols, db, db_fp32);
   count_launches(1);
   return cudaGetLastError();
 }
+
+int act_grad_blocks(long long n, int cols) { return actg::shape_of(n, cols).blocks; }
 
 }  // namespace prism

@@ -24,7 +24,7 @@
 // chain runs in the other accumulator.
 //
 // Roles (warps): 0 TMA producer, 1 MMA issuer (CTA 0 of a pair), 2 TMEM owner,
-// 3 producer of the codes (B8), 4-11 epilogue (two accumulators in TMEM alternate, so the epilogue of
+// 3 producer of the codes (B8) or the bias gradient's last step, 4-11 epilogue (two accumulators in TMEM alternate, so the epilogue of
 // one tile runs under the products of the next), from 12 the converters of B8.
 #pragma once
 
@@ -166,11 +166,37 @@ struct Args {
   long long ldy;
   uint16_t *Z;
   int out_fp32;
+  // the bias gradient's last step, by an idle warp: db = sums of `bias_blocks`
+  // rows of bias_part (db NULL: not asked of this launch)
+  const float *bias_part;
+  int bias_blocks, bias_cols;
+  void *db;
+  int db_fp32;
 };
 // The status word starts at 0 with the call's first kernel: cleared by its first
 // block, seconds before the shortest wait of any block can run out.
 __device__ __forceinline__ void reset_status(int *status, int reset) {
   if (reset && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) status[0] = status[1] = 0;
+}
+
+// db[c] = sum of part[0 .. blocks)[c], 32 columns a warp, in a fixed order: four
+// running sums of every fourth row, the odd rows on the first
+__device__ __forceinline__ void finish_bias(const float *part, int blocks, int cols, void *db, int fp32, int first, int step,
+                                            int lane) {
+  for (int c = first * 32 + lane; c < cols; c += step * 32) {
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    int b = 0;
+#pragma unroll 4
+    for (; b + 4 <= blocks; b += 4)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) a[k] += part[(long long)(b + k) * cols + c];
+    for (; b < blocks; ++b) a[0] += part[(long long)b * cols + c];
+    const float s = (a[0] + a[1]) + (a[2] + a[3]);
+    if (fp32)
+      static_cast<float *>(db)[c] = s;
+    else
+      static_cast<uint16_t *>(db)[c] = (uint16_t)(pack_bf16(s, s) & 0xffffu);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -812,6 +838,9 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
       if (lane == 0) drain_loads(bar.qfull, C::NQ, j, status, 414);
     }
     __syncwarp();
+  } else if (warp == 3) {
+    if (args.db)
+      finish_bias(args.bias_part, args.bias_blocks, args.bias_cols, args.db, args.db_fp32, blockIdx.x, gridDim.x, lane);
   } else if (warp >= 4 && warp < 4 + kEpiWarps) {
     // ---------------------------------------------------------------- epilogue
     if constexpr (C::B8) setmaxnreg_inc<C::SUM ? 144 : 128>();
@@ -986,6 +1015,9 @@ __global__ void __launch_bounds__(256, 2)
       bar.abort = 1;
       mma_drain(&bar.drain, status, 424);
     }
+  } else if (warp == 3) {
+    if (args.db)
+      finish_bias(args.bias_part, args.bias_blocks, args.bias_cols, args.db, args.db_fp32, blockIdx.x, gridDim.x, lane);
   } else if (warp >= 4) {
     // partial tile -> shared memory as [output row][output column]: plain, row-per-thread 16-byte units swizzled by
     // the row; swapped, a thread holds an output column, and neighbours' words are neighbours

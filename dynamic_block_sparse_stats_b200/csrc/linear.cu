@@ -269,9 +269,28 @@ static cudaError_t forward(const prism_linear_t &l, const uint16_t *X, long long
   return launch_plan<false, false>(p, m, a, st);
 }
 
+// The bias gradient's last step, for a launch to take along: its CTAs' idle warps
+// own 32 columns each, one round if there are as many CTAs.
+struct BiasTail {
+  const float *part;
+  int blocks, cols;
+  void *db;  // NULL: nothing (left) to do
+  int fp32;
+};
+static void take_bias(BiasTail &b, Args &a, int ctas) {
+  if (!b.db || (b.cols + 31) / 32 > ctas) return;
+  a.bias_part = b.part;
+  a.bias_blocks = b.blocks;
+  a.bias_cols = b.cols;
+  a.db = b.db;
+  a.db_fp32 = b.fp32;
+  b.db = nullptr;
+}
+static int ctas_of(const Plan &p) { return p.split ? p.s.tiles * p.split : p.s.groups * p.cg; }
+
 // dX [n][in] = dZ [n][out] W [out][in]
 static cudaError_t input_grad(const prism_linear_t &l, const uint16_t *dZ, long long ldd, const uint16_t *W,
-                              uint16_t *dX, int *status, int reset, cudaStream_t st) {
+                              uint16_t *dX, BiasTail &bias, int *status, int reset, cudaStream_t st) {
   const int rows = (int)l.n, cols = l.in;
   const Plan p = make_plan(rows, cols, (l.out + gemm::BK - 1) / gemm::BK, false, 1 << 30, true, false);
   Maps m;
@@ -285,6 +304,7 @@ static cudaError_t input_grad(const prism_linear_t &l, const uint16_t *dZ, long 
   a.cols = cols;
   a.status = status;
   a.reset = reset;
+  take_bias(bias, a, ctas_of(p));
   if (p.split) {
     a.Y = dX;
     a.ldy = cols;
@@ -311,7 +331,7 @@ static bool grad_restores(const prism_linear_t &l, const Plan &p) { return p.spl
 // dW [out][in] = dZ^T X, summed over the tokens
 static cudaError_t weight_grad(const prism_linear_t &l, const uint16_t *dZ, long long ldd, const uint16_t *X,
                                long long ldx, const prism_ckpt8_t *X8, uint16_t *restored, void *dW, int fp32,
-                               float *part, int *status, int reset, cudaStream_t st) {
+                               float *part, BiasTail &bias, int *status, int reset, cudaStream_t st) {
   const Plan p = grad_plan(l, fp32);
   cudaError_t e;
   if (X8 && grad_restores(l, p)) {
@@ -326,6 +346,7 @@ static cudaError_t weight_grad(const prism_linear_t &l, const uint16_t *dZ, long
   a.cols = l.in;
   a.status = status;
   a.reset = reset;
+  if (!X8) take_bias(bias, a, ctas_of(p));
   const int bm = 128 * p.cg;
   Maps m;
   if ((e = rows_map(&m.a, dZ, l.out, l.n, ldd, gemm::BK)) != cudaSuccess) return e;
@@ -535,10 +556,13 @@ int prism_linear_bwd(const prism_linear_t *l, const uint16_t *dY, int64_t lddy, 
     const uint16_t *dZ = act ? b.dZ : dY;
     const long long ldd = act ? l->out : lddy;
     const bool first = act || db;
-    if (first) e = launch_act_grad(l->n, l->out, l->act, dY, lddy, Z, ldz, Z8, b.dZ, b.bias_part, db, grad_fp32, status, st);
-    if (e == cudaSuccess && dX) e = input_grad(*l, dZ, ldd, W, dX, status, !first, st);
+    BiasTail bias = {b.bias_part, act_grad_blocks(l->n, l->out), l->out, db, grad_fp32};
+    if (first)
+      e = launch_act_grad(l->n, l->out, l->act, dY, lddy, Z, ldz, Z8, b.dZ, db ? b.bias_part : nullptr, status, st);
+    if (e == cudaSuccess && dX) e = input_grad(*l, dZ, ldd, W, dX, bias, status, !first, st);
     if (e == cudaSuccess && dW)
-      e = weight_grad(*l, dZ, ldd, X, ldx, X8, b.X, dW, grad_fp32, b.part, status, !first && !dX, st);
+      e = weight_grad(*l, dZ, ldd, X, ldx, X8, b.X, dW, grad_fp32, b.part, bias, status, !first && !dX, st);
+    if (e == cudaSuccess && bias.db) e = launch_bias_grad(l->n, l->out, b.bias_part, db, grad_fp32, st);
   }
   if (e != cudaSuccess) return refuse(PRISM_ERR_CUDA, "prism_linear_bwd: %s", cudaGetErrorString(e));
   clear_error();
