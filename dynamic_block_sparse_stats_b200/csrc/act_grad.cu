@@ -16,6 +16,15 @@ namespace actg {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
+// Rows in flight per thread, and the CTAs per SM that the registers must leave
+// room for.  Measured over 92160 x 4096 (gelu): bf16 Z, four rows 394 us, three
+// rows in four CTAs 368 (6.2 TB/s); checkpoint, four rows 353, six rows 326 (5.8
+// TB/s), eight 415.  Bound by memory, with the issue slots 60% busy.
+template <int ACT, bool Z8>
+struct Depth {
+  static constexpr bool kZ16 = ACT != PRISM_ACT_NONE && !Z8;
+  static constexpr int rows = kZ16 ? 3 : Z8 ? 6 : kUnroll, ctas = kZ16 ? 4 : 1;
+};
 
 // act'(z) of a pair in fp32, with p = 1 / (1 + e^-v).
 //   silu = z p(z):             slope p + z p (1 - p)
@@ -56,8 +65,9 @@ struct Src {
 
 // tx threads (a power of two, 8..32) cover 8 * tx columns of a row
 template <int ACT, bool Z8>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, (Depth<ACT, Z8>::ctas))
     act_grad_kernel(const Src s, long long n, int vecs, int tx, long long rows_per, float *__restrict__ part) {
+  constexpr int ROWS = Depth<ACT, Z8>::rows;
   __shared__ float red[kThreads][9];
   gemm::reset_status(s.status, 1);
   const int cx = threadIdx.x & (tx - 1), ry = threadIdx.x / tx, rows_step = kThreads / tx;
@@ -74,11 +84,11 @@ __global__ void __launch_bounds__(kThreads)
     uint4 *dz = s.dZ + r0 * vecs + cv;
     const long long dy_step = rows_step * s.ldy_vec, z_step = rows_step * s.ldz_vec, q_step = rows_step * (s.ldq >> 3),
                     s_step = rows_step * (s.ldq >> 5), dz_step = (long long)rows_step * vecs;
-    for (; left > 0; left -= kUnroll) {
-      uint4 d[kUnroll], z[kUnroll];
-      uint32_t sc[kUnroll];
+    for (; left > 0; left -= ROWS) {
+      uint4 d[ROWS], z[ROWS];
+      uint32_t sc[ROWS];
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
+      for (int u = 0; u < ROWS; ++u) {
         if (u < left) {
           d[u] = __ldcs(dy);
           dy += dy_step;
@@ -96,7 +106,7 @@ __global__ void __launch_bounds__(kThreads)
         }
       }
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
+      for (int u = 0; u < ROWS; ++u) {
         if (u >= left) break;
         const uint32_t dw[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
         if constexpr (ACT != PRISM_ACT_NONE) {

@@ -13,8 +13,8 @@
 // swizzled rows: K-major [rows][64 k], MN-major [64 k][64 mn] per 64 columns.
 //
 // B8: operand B (MN-major) is an 8-bit checkpoint (ckpt8.cu).  TMA brings the
-// codes, two teams of warps turn them into bf16 (exact: 8-bit integer times a power of
-// two) in the swizzled layout the tensor cores read.
+// codes, two teams of warps turn them into bf16 (exact: 8-bit integer times a
+// power of two) in the swizzled layout the tensor cores read.
 //
 // SUM: the tensor cores add into their fp32 accumulator with truncation, an
 // error that grows with the length of the chain (measured: 7e-8 of the sum's
@@ -24,8 +24,17 @@
 // chain runs in the other accumulator.
 //
 // Roles (warps): 0 TMA producer, 1 MMA issuer (CTA 0 of a pair), 2 TMEM owner,
-// 3 producer of the codes (B8) or the bias gradient's last step, 4-11 epilogue (two accumulators in TMEM alternate, so the epilogue of
-// one tile runs under the products of the next), from 12 the converters of B8.
+// 3 producer of the codes (B8) or the bias gradient's last step, 4-11 epilogue
+// (two accumulators in TMEM alternate, so the epilogue of one tile runs under the
+// products of the next), from 12 the converters of B8.
+//
+// What bounds it: a 256 x 256 pair tile takes 512 clocks of the tensor pipe a
+// stage and 32 KB into each CTA's shared memory, 64 bytes a clock, the most an SM
+// takes in from L2; measured, 0.40 us a stage.  In long runs the clock falls to
+// 1.3-1.6 GHz under the power cap.  92160 x 1024 x 1024 without epilogue work: 146
+// us, 1325 TFLOP/s (cuBLAS 138); with bias and residual 161, with bias and gelu
+// 155; 92160 x 4096 x 1024 (dX): 508 us, 1520 TFLOP/s.  A sixth stage in place of
+// the second staging buffers changed 1%, 128-column tiles run at half the rate.
 #pragma once
 
 #include "ckpt8.cuh"
@@ -38,9 +47,11 @@ namespace gemm {
 constexpr int BK = 64;  // contraction per stage: one 128-byte swizzle row of bf16
 constexpr int kEpiWarps = 8;
 constexpr int kStageBuf = 4096;  // one epilogue staging buffer: 32 rows x 128 bytes
-constexpr int kConvTeams = 2;  // teams of converter warps, taking the stages in turn
-constexpr int kConvTeam = 4;   // warps of a team
-constexpr int kChain = 8;  // stages per accumulator chain when SUM
+// Converters: two teams of four warps, which take the stages in turn (one team of
+// eight: 757 us at 92160 x 1024 x 4096, two of four 705, four of two 705).
+constexpr int kConvTeams = 2;
+constexpr int kConvTeam = 4;
+constexpr int kChain = 8;  // stages per accumulator chain when SUM: 5e-7 of the norm, 4% of the time
 
 template <int CG_, int BN_, bool A_MN_, bool B_MN_, bool B8_ = false, bool SUM_ = false>
 struct Cfg {
@@ -70,6 +81,7 @@ struct Cfg {
   static constexpr int THREADS = B8 ? 384 + 32 * kConvTeams * kConvTeam : 384;
   static_assert(SMEM <= 232448, "shared memory");
   static constexpr int TMEM_COLS = 2 * BN;
+  static_assert(BN == 128 || BN == 256, "each half of the epilogue warps owns one or two 64-column chunks");
   static_assert(!B8 || (B_MN && BNC == 128), "the checkpoint operand comes in 128-channel columns");
 };
 
@@ -437,16 +449,14 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
   const Sched &s = args.s;
   int *status = args.status;
   const int ew = warp - 4, q4 = warp & 3, half = ew >> 2;
-  constexpr int NCH = C::BN / 64;             // 64-column chunks of the tile
-  constexpr int PER = NCH > 1 ? NCH / 2 : 1;  // chunks of this warp
-  const int c_lo = NCH > 1 ? half * PER : 0;
-  const int n_ch = NCH > 1 ? PER : (half == 0 ? 1 : 0);
+  constexpr int n_ch = C::BN / 128;  // 64-column chunks of this warp: one or two
+  const int c_lo = half * n_ch;
   uint8_t *buf = staging + ew * C::NBUF * kStageBuf;
   const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
   const int sw = lane & 7;
   const bool z16 = args.save_z == 1;
   // codes through the second staging buffer; a single chunk's 64 bytes a row go straight to memory
-  const bool z8 = PER == 2 && C::NBUF == 2 && args.save_z == 2;
+  const bool z8 = n_ch == 2 && C::NBUF == 2 && args.save_z == 2;
   const bool solo = z16 || z8;  // the result has one buffer
   SegIter it(s, group);
   Seg sg;
@@ -472,7 +482,7 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
     if (args.has_res) {
       if (lane == 0) store_wait_read<0>();
       __syncwarp();
-      for (int c = 0; c < (solo ? min(n_ch, 1) : n_ch); ++c) load_res(c, c);
+      for (int c = 0; c < (solo ? 1 : n_ch); ++c) load_res(c, c);
     }
     const uint2 bias = load_bias(args.bias, n0, lane, min(args.cols, n0 + n_ch * 64));
     ok = __all_sync(0xffffffffu, mbar_wait(&bar.acc_full[ab], (t >> 1) & 1, status, 407));

@@ -444,9 +444,10 @@ size_t prism_linear_workspace_size(const prism_linear_t *l, int backward);
  * 16-byte aligned.  Other than R = Y, outputs may overlap no input.
  * Products are accumulated in fp32; bias, activation and residual are applied
  * in fp32, and Y (and Z) rounded to bf16 once.
- * Returns PRISM_OK, PRISM_ERR_INVALID_ARG, PRISM_ERR_CAPACITY or
- * PRISM_ERR_CUDA; a kernel that gives up on an internal wait records
- * PRISM_ERR_TIMEOUT in the workspace (prism_workspace_status).
+ * Returns PRISM_OK, PRISM_ERR_INVALID_ARG, PRISM_ERR_UNSUPPORTED (n * in or
+ * n * out too large), PRISM_ERR_CAPACITY or PRISM_ERR_CUDA; a kernel that gives
+ * up on an internal wait records PRISM_ERR_TIMEOUT in the workspace
+ * (prism_workspace_status).
  */
 int prism_linear_fwd(const prism_linear_t *l, const uint16_t *X, int64_t ldx,
                      const uint16_t *W, const uint16_t *bias, const uint16_t *R,

@@ -125,7 +125,7 @@ def test_backward(n, cin, cout, x8, act, z8):
         _check_bwd(d, g, act, x, z, fp32)
 
 
-@pytest.mark.parametrize("n,cin,cout", [(20000, 1024, 1024), (9000, 256, 2056), (70000, 264, 256)])
+@pytest.mark.parametrize("n,cin,cout", [(20000, 1024, 1024), (9000, 256, 2056), (9001, 712, 1000), (70000, 264, 256)])
 def test_large(n, cin, cout):
     """Several waves of the largest tiles, against float64 on the GPU: relative
     to the norm, one bf16 rounding of uniform relative error (2^-9 to 2^-8 at
@@ -272,6 +272,53 @@ def test_streams_and_graph():
     want_f = api.linear_fwd(d["X"], d["W"], d["b"], api.ACT_GELU, d["R"], "ckpt8")
     want_g = api.linear_bwd(d["dY"], d["X"], d["W"], want_f.Z, api.ACT_GELU)
     assert torch.equal(f.Y, want_f.Y) and all(torch.equal(getattr(g, k), getattr(want_g, k)) for k in ("dX", "dW", "db"))
+
+
+def test_two_graphs_replayed_in_turn_and_at_once():
+    """Two captured training steps, each with its own buffers, replayed on two
+    streams at once give what eager calls give."""
+    runs = []
+    for seed in (31, 32):
+        d = _inputs(2300, 520, 640, seed=seed)
+
+        def step(d=d):
+            x8 = api.ckpt8_pack(d["X"])
+            f = api.linear_fwd(d["X"], d["W"], d["b"], api.ACT_GELU, d["R"], "ckpt8")
+            return f, api.linear_bwd(d["dY"], x8, d["W"], f.Z, api.ACT_GELU)
+
+        want = step()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = step()
+        runs.append((g, got, want, d))              # a graph does not keep its inputs
+    streams = [torch.cuda.Stream() for _ in runs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for (g, _, _, _), s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, (f, b), (wf, wb), _ in runs:
+        assert api.workspace_status(f.ws) == 0 and api.workspace_status(b.ws) == 0
+        assert torch.equal(f.Y, wf.Y) and all(torch.equal(getattr(b, k), getattr(wb, k)) for k in ("dX", "dW", "db"))
+
+
+def test_a_workspace_is_used_again():
+    """One workspace buffer for calls of different sizes, one after the other on a
+    stream, whatever it held before; its status word starts clear in each."""
+    ws = torch.full((api.linear_workspace_size(3000, 512, 512, api.ACT_GELU, True, x8=True),), 0xff, dtype=torch.uint8,
+                    device="cuda")
+    for n, cin, cout in ((3000, 512, 512), (5, 64, 72), (700, 264, 512)):
+        d = _inputs(n, cin, cout)
+        f = api.linear_fwd(d["X"], d["W"], d["b"], api.ACT_GELU, save="ckpt8", ws=ws)
+        assert api.workspace_status(ws) == 0
+        x8 = api.ckpt8_pack(d["X"])
+        for need in (("dX", "dW", "db"), ("dX",), ("dW",), ("db",)):
+            ws[:256] = 0xff
+            g = api.linear_bwd(d["dY"], x8, d["W"], f.Z, api.ACT_GELU, need=need, ws=ws)
+            assert api.workspace_status(ws) == 0
+            want = api.linear_bwd(d["dY"], x8, d["W"], f.Z, api.ACT_GELU, need=need)
+            assert all(torch.equal(getattr(g, k), getattr(want, k)) for k in need)
 
 
 def test_non_finite_inputs_stay_in_their_rows():

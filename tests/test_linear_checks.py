@@ -48,6 +48,13 @@ def test_bad_descriptions(kw):
     assert lib.prism_linear_workspace_size(None, 0) == 0
 
 
+def test_sizes_past_2_40_values():
+    big = _lin(n=(1 << 30) - 8, i=64, o=1 << 16)
+    assert _lib.load().prism_linear_workspace_size(big, 1) == 0
+    assert _fwd(big, ldy=1 << 16) == _lib.PRISM_ERR_UNSUPPORTED
+    assert _bwd(big, lddy=1 << 16) == _lib.PRISM_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("kw", [dict(X=None), dict(W=None), dict(Y=None), dict(ldx=56), dict(ldx=68), dict(ldy=120),
                                 dict(ldy=132), dict(X=C.c_void_p(264)), dict(W=C.c_void_p(264)), dict(bias=C.c_void_p(264)),
                                 dict(Y=C.c_void_p(264)), dict(R=OK, ldr=64), dict(R=C.c_void_p(258), ldr=128),
