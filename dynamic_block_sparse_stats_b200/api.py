@@ -572,7 +572,11 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
     if bias is not None:
         _check_tensor(bias, "bias", torch.bfloat16, (cout,))
     ldr = _check_rows(residual, "residual", (n, cout)) if residual is not None else 0
-    ldy = _check_rows(Y, "Y", (n, cout)) if Y is not None else cout
+    ldy = cout
+    if Y is not None:
+        ldy = _check_rows(Y, "Y", (n, cout))
+        if n > 0 and Y.data_ptr() == X.data_ptr():
+            raise ValueError("Y may not be X (every output channel reads all of X's)")
     if save not in (None, "bf16", "ckpt8"):
         raise ValueError(f'save must be None, "bf16" or "ckpt8", got {save!r}')
     if Z is not None:
@@ -660,6 +664,8 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
                     raise ValueError(f"out holds {name}, which need does not name")
                 _check_tensor(t, name, dtype, shape)
                 named.append((name, t))
+        if dX is not None and n > 0 and dX.data_ptr() == dY.data_ptr():
+            raise ValueError("dX may not be dY (every input channel reads all of dY's)")
     if ws is not None:
         _check_workspace(ws, "ws")
         named.append(("ws", ws))

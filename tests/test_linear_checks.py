@@ -114,6 +114,27 @@ def _t(*shape, dtype=torch.bfloat16):
     return torch.zeros(*shape, dtype=dtype)
 
 
+def _same(n=4, c=8):
+    t = _t(n, c)
+    return t, t
+
+
+def _fwd_onto_itself():
+    x, y = _same()
+    return api.linear_fwd(x, _t(8, 8), Y=y)
+
+
+def _bwd_onto_itself():
+    dy, dx = _same()
+    return api.linear_bwd(dy, _t(4, 8), _t(8, 8), out=(dx, None, None))
+
+
+def test_outputs_onto_inputs_are_refused():
+    for call in (_fwd_onto_itself, _bwd_onto_itself):
+        with pytest.raises(ValueError, match="may not be"):
+            call()
+
+
 @pytest.mark.parametrize("make,err", [
     (lambda: api.linear_fwd(_t(4, 8), _t(16, 16)), ValueError),
     (lambda: api.linear_fwd(_t(4, 8, dtype=torch.float32), _t(16, 8)), ValueError),
