@@ -961,7 +961,25 @@ __global__ void __launch_bounds__(256, 2)
   int *status = args.status;
   reset_status(status, args.reset);
 
+  const auto load_stage = [&](int j) {
+    const int st = j % NST, k = k0 + j;
+    uint8_t *a = smem + st * L::STAGE, *b = a + L::A_BYTES;
+    mbar_arrive_expect_tx(&bar.full[st], L::STAGE);
+    if constexpr (A_MN) {
+      tma_load_2d(a, &mapA, &bar.full[st], m0, k * BK);
+      tma_load_2d(a + BK * 128, &mapA, &bar.full[st], m0 + 64, k * BK);
+    } else {
+      tma_load_2d(a, &mapA, &bar.full[st], k * BK, m0);
+    }
+    if constexpr (B_MN)
+      tma_load_2d(b, &mapB, &bar.full[st], n0, k * BK);
+    else
+      tma_load_2d(b, &mapB, &bar.full[st], k * BK, n0);
+  };
+  const int first = min(NST, k1 - k0);  // stages that travel while the rest of the block sets up
   if (threadIdx.x == 0) {
+    prefetch_tensormap(&mapA);
+    prefetch_tensormap(&mapB);
     for (int i = 0; i < NST; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
@@ -970,6 +988,8 @@ __global__ void __launch_bounds__(256, 2)
     mbar_init(&bar.drain, 1);
     bar.abort = 0;
     fence_barrier_init();
+    fence_async_smem();
+    for (int j = 0; j < first; ++j) load_stage(j);
   }
   if (warp == 2) tmem_alloc_g<1>(&bar.tmem_base, 64);
   tc_fence_before();
@@ -979,26 +999,15 @@ __global__ void __launch_bounds__(256, 2)
 
   if (warp == 0 && lane == 0) {
     bool ok = true;
-    int j = 0;
-    for (int k = k0; k < k1; ++k, ++j) {
+    int j = first;
+    for (; j < k1 - k0; ++j) {
       const int st = j % NST;
-      if (j >= NST && !(ok = mbar_wait(&bar.empty[st], ((j / NST) - 1) & 1, status, 421))) break;
+      if (!(ok = mbar_wait(&bar.empty[st], ((j / NST) - 1) & 1, status, 421))) break;
       if (*reinterpret_cast<volatile int *>(&bar.abort)) {
         ok = false;
         break;
       }
-      uint8_t *a = smem + st * L::STAGE, *b = a + L::A_BYTES;
-      mbar_arrive_expect_tx(&bar.full[st], L::STAGE);
-      if constexpr (A_MN) {
-        tma_load_2d(a, &mapA, &bar.full[st], m0, k * BK);
-        tma_load_2d(a + BK * 128, &mapA, &bar.full[st], m0 + 64, k * BK);
-      } else {
-        tma_load_2d(a, &mapA, &bar.full[st], k * BK, m0);
-      }
-      if constexpr (B_MN)
-        tma_load_2d(b, &mapB, &bar.full[st], n0, k * BK);
-      else
-        tma_load_2d(b, &mapB, &bar.full[st], k * BK, n0);
+      load_stage(j);
     }
     if (!ok) bar.abort = 1;
     drain_loads(bar.full, NST, j, status, 422);
