@@ -618,9 +618,9 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
     is dY itself."""
     lddy = _check_rows(dY, "dY")
     n, cout = dY.shape
-    if not need or not all(k in ("dX", "dW", "db") for k in need):
-        raise ValueError(f'need must name some of "dX", "dW", "db", got {need!r}')
     want_x, want_w, want_b = "dX" in need, "dW" in need, "db" in need
+    if isinstance(need, str) or len(need) == 0 or len(need) != want_x + want_w + want_b:
+        raise ValueError(f'need must name some of "dX", "dW", "db", once each, got {need!r}')
     if want_x and W is None:
         raise ValueError("dX needs W")
     if want_w and X is None:
