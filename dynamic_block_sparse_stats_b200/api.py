@@ -631,8 +631,11 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
             raise ValueError("W must be a 2-D tensor [out, in]")
         cin = W.shape[1]
         _check_tensor(W, "W", torch.bfloat16, (cout, cin))
+    elif x8:
+        cin = X.width
     elif X is not None:
-        cin = X.width if x8 else X.shape[-1]
+        _check_rows(X, "X")
+        cin = X.shape[1]
     else:
         cin = 8  # only db: the input's width does not matter
     named = [("dY", dY), ("W", W)]

@@ -324,8 +324,8 @@ static size_t grad_part_bytes(const Plan &p) {
 // A checkpointed X is converted on its way to the tensor cores, once for every
 // 256 output channels.  From 2048 of them on, restoring it once is faster, and
 // so it is for the small tiles, whose kernels read bf16 only.  Measured at
-// 92160 x 1024: out = 1024, 185 us against 53 + 155; out = 4096, 703 against
-// 53 + 553.
+// 92160 x 1024 in long runs, converted against restored (us): out = 512, 135 and
+// 172; 1024, 251 and 268; 2048, 464 and 434.
 static bool grad_restores(const prism_linear_t &l, const Plan &p) { return p.split || p.cg == 1 || l.out >= 2048; }
 
 // dW [out][in] = dZ^T X, summed over the tokens

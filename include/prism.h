@@ -374,8 +374,9 @@ int prism_attn_bwd(const prism_params *p, const prism_plan_t *plan,
  * An activation checkpoint in 8 bits: a matrix [n][width] held as signed 8-bit
  * codes and, for every block of 32 channels of a row, one power-of-two scale.
  *   codes   int8 [n][ld]; channels at index >= width hold 0.  16-byte aligned.
- *   scales  uint8 [n][ld / 32]: scale byte s stands for 2^(s - 127).  4-byte
- *           aligned.  Blocks that start at or beyond width are unspecified.
+ *   scales  uint8 [n][ld / 32]: scale byte s stands for 2^(s - 127), 1 <= s <= 248
+ *           or 255 (not a number; see below).  4-byte aligned.  Blocks that
+ *           start at or beyond width are unspecified.
  *   ld      width rounded up to a multiple of 128.
  * The value of a channel is code * 2^(s - 127), exact in bf16.  s is the
  * smallest integer >= 1 with max|x| <= 127 * 2^(s - 127) over the block, and

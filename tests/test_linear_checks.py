@@ -154,6 +154,8 @@ def test_outputs_onto_inputs_are_refused():
     (lambda: api.linear_bwd(_t(4, 16), _t(4, 8), _t(8, 16)), ValueError),
     (lambda: api.linear_bwd(_t(4, 16), _t(5, 8), _t(16, 8)), ValueError),
     (lambda: api.linear_bwd(_t(4, 16), None, _t(16, 8)), ValueError),
+    (lambda: api.linear_bwd(_t(4, 16), [[1.0]], None, need=("dW",)), TypeError),
+    (lambda: api.linear_bwd(_t(4, 16), _t(4, 8), _t(16, 8), need=("dX", "dX")), ValueError),
     (lambda: api.linear_bwd(_t(4, 16), _t(4, 8), None), ValueError),
     (lambda: api.linear_bwd(_t(4, 16), _t(4, 8), _t(16, 8), act=api.ACT_GELU), ValueError),
     (lambda: api.linear_bwd(_t(4, 16), _t(4, 8), _t(16, 8), _t(4, 8), api.ACT_GELU), ValueError),
