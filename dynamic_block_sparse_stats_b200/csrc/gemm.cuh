@@ -24,17 +24,18 @@
 // chain runs in the other accumulator.
 //
 // Roles (warps): 0 TMA producer, 1 MMA issuer (CTA 0 of a pair), 2 TMEM owner,
-// 3 producer of the codes (B8) or the bias gradient's last step, 4-11 epilogue
-// (two accumulators in TMEM alternate, so the epilogue of one tile runs under the
-// products of the next), from 12 the converters of B8.
+// 3 producer of the codes (B8) or the bias gradient's last step, from 4 on the
+// epilogue (two accumulators in TMEM alternate, so the epilogue of one tile runs
+// under the products of the next), then the converters of B8.
 //
 // What bounds it: a 256 x 256 pair tile takes 512 clocks of the tensor pipe a
 // stage and 32 KB into each CTA's shared memory, 64 bytes a clock, the most an SM
 // takes in from L2; measured, 0.40 us a stage.  In long runs the clock falls to
-// 1.3-1.6 GHz under the power cap.  92160 x 1024 x 1024 without epilogue work: 146
-// us, 1325 TFLOP/s (cuBLAS 138); with bias and residual 161, with bias and gelu
-// 155; 92160 x 4096 x 1024 (dX): 508 us, 1520 TFLOP/s.  A sixth stage in place of
-// the second staging buffers changed 1%, 128-column tiles run at half the rate.
+// 1.3-1.6 GHz under the power cap.  92160 x 1024 x 1024 without epilogue work: 144
+// us, 1340 TFLOP/s (cuBLAS 138); with bias and residual 161, with bias and gelu
+// 156; 92160 x 4096 x 1024 (dX): 508 us, 1520 TFLOP/s.  The sixth stage, in place
+// of a second staging buffer per warp, gave 3%; 128-column tiles run at half the
+// rate.
 #pragma once
 
 #include "ckpt8.cuh"
@@ -45,15 +46,14 @@ namespace prism {
 namespace gemm {
 
 constexpr int BK = 64;  // contraction per stage: one 128-byte swizzle row of bf16
-constexpr int kEpiWarps = 8;
-constexpr int kStageBuf = 4096;  // one epilogue staging buffer: 32 rows x 128 bytes
+constexpr int kStageBuf = 4096;  // an epilogue warp's staging buffer: 32 rows x 128 bytes
 // Converters: two teams of four warps, which take the stages in turn (one team of
 // eight: 757 us at 92160 x 1024 x 4096, two of four 705, four of two 705).
 constexpr int kConvTeams = 2;
 constexpr int kConvTeam = 4;
 constexpr int kChain = 8;  // stages per accumulator chain when SUM: 5e-7 of the norm, 4% of the time
 
-template <int CG_, int BN_, bool A_MN_, bool B_MN_, bool B8_ = false, bool SUM_ = false>
+template <int CG_, int BN_, bool A_MN_, bool B_MN_, bool B8_ = false, bool SUM_ = false, int EW_ = 8>
 struct Cfg {
   static constexpr int CG = CG_, BN = BN_;
   static constexpr bool A_MN = A_MN_, B_MN = B_MN_, B8 = B8_, SUM = SUM_;
@@ -65,8 +65,14 @@ struct Cfg {
   // rings of operand stages: A with B; with B8 three of their own, so that the
   // codes arrive and are converted well ahead of the products
   static constexpr int STAGE = B8 ? A_BYTES : A_BYTES + B_BYTES;
-  static constexpr int NBUF = B8 ? 1 : 2;  // staging buffers of an epilogue warp
-  static constexpr int EPI = kEpiWarps * NBUF * kStageBuf;
+  // Epilogue warps: 8, which leave room for a sixth stage; or 16, one 64-column
+  // chunk each of 256 columns, which hide one another's latencies and the
+  // exponentials' (wide_epilogue in linear.cu says when).
+  static constexpr int EW = EW_;
+  // 128-column tiles stage a saved pre-activation in a buffer of its own; the others
+  // have no room for one and take a second pass over the accumulator
+  static constexpr int NBUF = BN == 128 ? 2 : 1;
+  static constexpr int EPI = EW * NBUF * kStageBuf;
   static constexpr int NST_FIT = (232448 - 2048 - EPI) / STAGE;
   static constexpr int NST = B8 ? 5 : NST_FIT < 6 ? NST_FIT : 6;
   static constexpr int NB = B8 ? 4 : NST;
@@ -78,10 +84,12 @@ struct Cfg {
   static constexpr int OFF_BAR = OFF_EPI + EPI;
   static constexpr int OFF_SC = OFF_BAR + 1024;        // B8: scale words of the codes' stages, one per token
   static constexpr int SMEM = OFF_SC + (B8 ? NQ * BK * 4 : 0) + 1024;  // slack to align the base to 1024
-  static constexpr int THREADS = B8 ? 384 + 32 * kConvTeams * kConvTeam : 384;
+  static constexpr int THREADS = 128 + 32 * EW + (B8 ? 32 * kConvTeams * kConvTeam : 0);
+  static constexpr bool REGS = THREADS == 640;  // registers move between warpgroups
   static_assert(SMEM <= 232448, "shared memory");
   static constexpr int TMEM_COLS = 2 * BN;
-  static_assert(BN == 128 || BN == 256, "each half of the epilogue warps owns one or two 64-column chunks");
+  static_assert(EW == 8 || (EW == 16 && BN == 256 && !B8 && !SUM), "epilogue warps");
+  static_assert(BN / 64 % (EW / 4) == 0, "each four epilogue warps own whole 64-column chunks");
   static_assert(!B8 || (B_MN && BNC == 128), "the checkpoint operand comes in 128-channel columns");
 };
 
@@ -90,7 +98,7 @@ struct Bars {
   uint64_t bfull[6], bempty[6];        // B8: B converted (CTA 0's), consumed (each CTA's own)
   uint64_t qfull[6], qempty[6];        // B8: codes arrived, converted (each CTA's own)
   uint64_t acc_full[2], acc_empty[2];  // accumulators: complete (each CTA's own), read (CTA 0's)
-  uint64_t res[kEpiWarps][2];          // residual tiles of each epilogue warp
+  uint64_t res[16];                    // residual tiles of each epilogue warp
   uint64_t drain;                      // single use, after an abort
   uint32_t tmem_base;
   int abort;
@@ -378,7 +386,7 @@ __device__ __forceinline__ uint4 pack8(const float2 (&v)[16], int i) {
                     pack_bf16(v[i + 3].x, v[i + 3].y));
 }
 
-// The bias of a warp's (at most 128) columns, four to a lane, loaded while the
+// The bias of a warp's 64 columns, four to a lane of the first sixteen, loaded while the
 // products still run; add_bias hands a group of 32 columns round by shuffles.
 __device__ __forceinline__ uint2 load_bias(const uint16_t *bias, int c0, int lane, int cols) {
   const int c = c0 + lane * 4;
@@ -404,18 +412,6 @@ __device__ __forceinline__ void apply_act(float2 (&v)[16], int act) {
       break;
   }
 }
-// the block's checkpoint; returns its scale byte
-__device__ __forceinline__ uint32_t save_codes(const float2 (&v)[16], const Args &args, int row, int c0) {
-  uint32_t q[8];
-  const uint32_t sc = ckpt8_quantise(v, q);
-  if (row < args.rows && c0 < args.ldq) {
-    uint4 *dst = reinterpret_cast<uint4 *>(args.codes + (long long)row * args.ldq + c0);
-    dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
-    dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
-  }
-  return sc;
-}
-
 // one warp's 32 x 32 fp32 values (thread = row) through a staging buffer to
 // column x, row y of `map`
 __device__ __forceinline__ void stage_fp32(const CUtensorMap *map, uint8_t *buf, const uint32_t (&v)[32], int lane, int x,
@@ -435,12 +431,11 @@ __device__ __forceinline__ void stage_fp32(const CUtensorMap *map, uint8_t *buf,
 
 // A tile of D straight from its accumulator: bias, saved pre-activation,
 // activation and residual, rounded to bf16; or fp32 partial sums of a split
-// tile.  Each of the eight warps has two 4 KB staging buffers (32 rows x 64
-// bf16, 128-byte swizzled as the tensor maps are), one for each of the at most
-// two 64-column chunks it owns: a buffer receives its chunk's residual by TMA
-// while the products run, then the result, then feeds the TMA store.  When the
-// pre-activation is saved, it takes the second buffer: in bf16 chunk by chunk, as
-// codes (128 bytes a row) for both chunks at once.
+// tile.  Each warp owns 32 rows of one 64-column chunk, or of two one after the
+// other, and a 4 KB staging buffer, 128-byte swizzled as the tensor maps are: it
+// receives the chunk's residual by TMA while the products run, then the result,
+// then feeds the TMA store.  A saved pre-activation has a second buffer, or goes
+// through the first one before, in a pass of its own over the accumulator.
 template <class C>
 __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUtensorMap &mapR, const CUtensorMap &mapZ,
                                               const Args &args, Bars &bar, uint8_t *staging, uint32_t tmem, int group,
@@ -448,120 +443,129 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
   constexpr int CG = C::CG;
   const Sched &s = args.s;
   int *status = args.status;
-  const int ew = warp - 4, q4 = warp & 3, half = ew >> 2;
-  constexpr int n_ch = C::BN / 128;  // 64-column chunks of this warp: one or two
-  const int c_lo = half * n_ch;
+  const int ew = warp - 4, q4 = warp & 3;
   uint8_t *buf = staging + ew * C::NBUF * kStageBuf;
+  uint8_t *row = buf + lane * 128;
+  uint8_t *zbuf = buf + (C::NBUF - 1) * kStageBuf;
   const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
   const int sw = lane & 7;
-  const bool z16 = args.save_z == 1;
-  // codes through the second staging buffer; a single chunk's 64 bytes a row go straight to memory
-  const bool z8 = n_ch == 2 && C::NBUF == 2 && args.save_z == 2;
-  const bool solo = z16 || z8;  // the result has one buffer
   SegIter it(s, group);
   Seg sg;
   int t = 0;
-  uint32_t res_phase = 0;  // bit i: parity of the next wait on residual buffer i
+  uint32_t res_phase = 0;
   bool ok = true;
   for (; ok && it.next(s, sg); ++t) {
     const int ab = t & 1;
     const int m0 = (sg.tile / s.tiles_n) * C::BM + rank * 128 + q4 * 32;
-    const int n0 = (sg.tile % s.tiles_n) * C::BN + c_lo * 64;
     const bool parts = sg.slot >= 0;
     const bool rows_in = m0 < args.rows;
-    uint32_t res_pending = 0;
-    // residual of chunk c into buffer b (its last store has been read)
-    const auto load_res = [&](int c, int b) {
-      if (!(args.has_res && rows_in && n0 + c * 64 < args.cols)) return;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bar.res[ew][b], kStageBuf);
-        tma_load_2d(buf + b * kStageBuf, &mapR, &bar.res[ew][b], n0 + c * 64, m0);
-      }
-      res_pending |= 1u << b;
-    };
-    if (args.has_res) {
+    bool res_pending = false;
+    // the buffer's last store has been read
+    const auto free_buffer = [&] {
       if (lane == 0) store_wait_read<0>();
       __syncwarp();
-      for (int c = 0; c < (solo ? 1 : n_ch); ++c) load_res(c, c);
+    };
+    const auto load_res = [&](int col0) {
+      if (!(args.has_res && rows_in && col0 < args.cols)) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&bar.res[ew], kStageBuf);
+        tma_load_2d(buf, &mapR, &bar.res[ew], col0, m0);
+      }
+      res_pending = true;
+    };
+    const int n0 = (sg.tile % s.tiles_n) * C::BN;
+    const int c_first = ew >> 2;
+    if (!parts) {
+      free_buffer();
+      if (C::NBUF == 2 || !args.save_z) load_res(n0 + c_first * 64);
     }
-    const uint2 bias = load_bias(args.bias, n0, lane, min(args.cols, n0 + n_ch * 64));
     ok = __all_sync(0xffffffffu, mbar_wait(&bar.acc_full[ab], (t >> 1) & 1, status, 407));
     if (ok) {
       tc_fence_after();
-      const uint32_t acc = tmem + ab * C::BN + c_lo * 64 + lane_off;
-      uint32_t scale4 = 0;
-      if (parts) {
-        if (lane == 0) store_wait_read<0>();
-        __syncwarp();
 #pragma unroll 1
-        for (int g = 0; g < 2 * n_ch; ++g) {
-          uint32_t v[32];
-          tmem_ld32(acc + g * 32, v);
-          tmem_wait_ld();
-          if (lane == 0) store_wait_read<C::NBUF - 1>();
-          __syncwarp();
-          stage_fp32(&mapZ, buf + (g & (C::NBUF - 1)) * kStageBuf, v, lane, c_lo * 64 + g * 32,
-                     sg.slot * C::BM + rank * 128 + q4 * 32, true);
-        }
-      }
-#pragma unroll 1
-      for (int c = 0; c < (parts ? 0 : n_ch); ++c) {
+      for (int c = c_first; c < C::BN / 64; c += C::EW / 4) {
         const int col0 = n0 + c * 64;
-        const bool in = rows_in && col0 < args.cols;
-        const int yb = solo || C::NBUF == 1 ? 0 : c;
-        if (solo && c > 0) {
-          if (lane == 0) store_wait_read<0>();
-          __syncwarp();
-          load_res(c, 0);
-        }
-        const bool res = (res_pending >> yb) & 1;
-        if (!args.has_res) {
-          // this buffer's last store was the one before the last (solo: the last)
-          if (lane == 0) {
-            if (solo || C::BN < 256 || C::NBUF == 1)
-              store_wait_read<0>();
-            else
-              store_wait_read<1>();
-          }
-          __syncwarp();
-        }
-        if (!z8 || c == 0) scale4 = 0;
-        uint8_t *row = buf + yb * kStageBuf + lane * 128;
+        const uint32_t acc = tmem + ab * C::BN + c * 64 + lane_off;
+        if (parts) {
 #pragma unroll 1
-        for (int g = 0; g < 2; ++g) {
-          const int cg0 = col0 + g * 32;
+          for (int g = 0; g < 2; ++g) {
+            uint32_t v[32];
+            tmem_ld32(acc + g * 32, v);
+            tmem_wait_ld();
+            free_buffer();
+            stage_fp32(&mapZ, buf, v, lane, c * 64 + g * 32, sg.slot * C::BM + rank * 128 + q4 * 32, true);
+          }
+          continue;
+        }
+        const bool in = rows_in && col0 < args.cols;
+        const uint2 bias = load_bias(args.bias, col0, lane, min(args.cols, col0 + 64));
+        // 32 columns of the pre-activation
+        const auto pre = [&](int g, float2 (&v)[16]) {
           uint32_t u[32];
-          tmem_ld32(acc + c * 64 + g * 32, u);
+          tmem_ld32(acc + g * 32, u);
           tmem_wait_ld();
-          float2 v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-          if (args.bias) add_bias(v, bias, 2 * c + g);
-          if (z16) {
+          if (args.bias) add_bias(v, bias, g);
+        };
+        uint32_t scale2 = 0;
+        // 32 columns of Z into its staging buffer
+        const auto stage_z = [&](int g, const float2 (&v)[16]) {
+          if (args.save_z == 1) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4 *>(row + kStageBuf + (((g * 4 + i) ^ sw) << 4)) = pack8(v, 4 * i);
-          } else if (z8) {
+              *reinterpret_cast<uint4 *>(zbuf + lane * 128 + (((g * 4 + i) ^ sw) << 4)) = pack8(v, 4 * i);
+          } else {
+            // 64 bytes a row, 64-byte swizzled
             uint32_t q[8];
-            scale4 |= ckpt8_quantise(v, q) << (8 * (2 * c + g));
-            uint8_t *qrow = buf + kStageBuf + lane * 128;
-            const int u0 = 4 * c + 2 * g;
-            *reinterpret_cast<uint4 *>(qrow + ((u0 ^ sw) << 4)) = make_uint4(q[0], q[1], q[2], q[3]);
-            *reinterpret_cast<uint4 *>(qrow + (((u0 + 1) ^ sw) << 4)) = make_uint4(q[4], q[5], q[6], q[7]);
-          } else if (args.save_z == 2) {
-            scale4 |= save_codes(v, args, m0 + lane, cg0) << (8 * g);
+            scale2 |= ckpt8_quantise(v, q) << (8 * g);
+            uint8_t *qrow = zbuf + lane * 64;
+            const int x = (lane >> 1) & 3;
+            *reinterpret_cast<uint4 *>(qrow + (((2 * g) ^ x) << 4)) = make_uint4(q[0], q[1], q[2], q[3]);
+            *reinterpret_cast<uint4 *>(qrow + (((2 * g + 1) ^ x) << 4)) = make_uint4(q[4], q[5], q[6], q[7]);
           }
+        };
+        const auto store_z = [&] {  // by lane 0, after the fence
+          if (rows_in && col0 < (args.save_z == 2 ? (int)args.ldq : args.cols)) store_2d(&mapZ, zbuf, col0, m0);
+        };
+        const auto store_scales = [&] {
+          if (args.save_z == 2 && m0 + lane < args.rows && col0 < args.ldq)
+            *reinterpret_cast<uint16_t *>(args.scales + (long long)(m0 + lane) * (args.ldq / 32) + col0 / 32) =
+                (uint16_t)scale2;
+        };
+        if (C::NBUF == 1 && args.save_z) {
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {
+            float2 v[16];
+            pre(g, v);
+            stage_z(g, v);
+          }
+          store_scales();
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            store_z();
+            store_commit();
+          }
+          free_buffer();
+          load_res(col0);
+        }
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          float2 v[16];
+          pre(g, v);
+          if (C::NBUF == 2 && args.save_z) stage_z(g, v);
           apply_act(v, args.act);
-          if (res && g == 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&bar.res[ew][yb], (res_phase >> yb) & 1, status, 408));
-            res_phase ^= 1u << yb;
-            res_pending &= ~(1u << yb);
+          if (g == 0 && res_pending) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bar.res[ew], res_phase, status, 408));
+            res_phase ^= 1;
+            res_pending = false;
             if (!ok) break;
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint4 *p = reinterpret_cast<uint4 *>(row + (((g * 4 + i) ^ sw) << 4));
-            if (res) {
+            if (args.has_res && in) {
               const uint4 r = *p;
               const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -571,22 +575,17 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
           }
         }
         if (!ok) break;
-        if (args.save_z == 2 && m0 + lane < args.rows && col0 < args.ldq) {
-          uint8_t *sp = args.scales + (long long)(m0 + lane) * (args.ldq / 32) + col0 / 32;
-          if (!z8)
-            *reinterpret_cast<uint16_t *>(sp) = (uint16_t)scale4;
-          else if (c == 1)
-            *reinterpret_cast<uint32_t *>(sp - 2) = scale4;
-        }
+        if (C::NBUF == 2 && args.save_z) store_scales();
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (in) {
-            store_2d(&mapY, buf + yb * kStageBuf, col0, m0);
-            if (z16) store_2d(&mapZ, buf + kStageBuf, col0, m0);
-          }
-          if (z8 && c == 1 && rows_in && n0 < args.ldq) store_2d(&mapZ, buf + kStageBuf, n0, m0);
+          if (in) store_2d(&mapY, buf, col0, m0);
+          if (C::NBUF == 2 && args.save_z) store_z();
           store_commit();
+        }
+        if (c + C::EW / 4 < C::BN / 64) {
+          free_buffer();
+          if (C::NBUF == 2 || !args.save_z) load_res(col0 + C::EW / 4 * 64);
         }
       }
       tc_fence_before();
@@ -595,22 +594,21 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
     }
     if (!ok) {
       bar.abort = 1;
-      for (int b = 0; b < 2; ++b)  // loads that nothing will read
-        if ((res_pending >> b) & 1) mbar_wait(&bar.res[ew][b], (res_phase >> b) & 1, status, 409);
+      if (res_pending) mbar_wait(&bar.res[ew], res_phase, status, 409);  // a load that nothing will read
     }
   }
   if (lane == 0) store_wait_read<0>();
 }
 
 // SUM: the chains of a segment added up in registers (a thread's row x its
-// half of the columns), then written in fp32: a whole tile to the output, a
+// warp's columns), then written in fp32: a whole tile to the output, a
 // partial one to its slot.
 template <class C>
 __device__ __forceinline__ void epilogue_sum(const CUtensorMap &mapY, const CUtensorMap &mapZ, const Args &args, Bars &bar,
                                              uint8_t *staging, uint32_t tmem, int group, int rank, int warp, int lane) {
   const Sched &s = args.s;
   const int ew = warp - 4, q4 = warp & 3, half = ew >> 2;
-  constexpr int COLS = C::BN / 2;
+  constexpr int COLS = C::BN / (C::EW / 4);  // this warp's columns
   uint8_t *buf = staging + ew * C::NBUF * kStageBuf;
   const uint32_t acc0 = tmem + half * COLS + ((uint32_t)(q4 * 32) << 16);
   SegIter it(s, group);
@@ -643,16 +641,16 @@ __device__ __forceinline__ void epilogue_sum(const CUtensorMap &mapY, const CUte
     const int n0 = (sg.tile % s.tiles_n) * C::BN + half * COLS;
 #pragma unroll
     for (int g = 0; g < COLS / 32; ++g) {
-      if (lane == 0) store_wait_read<C::NBUF - 1>();
+      if (lane == 0) store_wait_read<0>();
       __syncwarp();
       uint32_t v[32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[g * 32 + i]);
       if (sg.slot >= 0)
-        stage_fp32(&mapZ, buf + (g & (C::NBUF - 1)) * kStageBuf, v, lane, half * COLS + g * 32,
+        stage_fp32(&mapZ, buf, v, lane, half * COLS + g * 32,
                    sg.slot * C::BM + rank * 128 + q4 * 32, true);
       else
-        stage_fp32(&mapY, buf + (g & (C::NBUF - 1)) * kStageBuf, v, lane, n0 + g * 32, m0,
+        stage_fp32(&mapY, buf, v, lane, n0 + g * 32, m0,
                    m0 < args.rows && n0 + g * 32 < args.cols);
     }
   }
@@ -690,10 +688,9 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.acc_full[i], 1);
-      mbar_init(&bar.acc_empty[i], kEpiWarps * CG);
+      mbar_init(&bar.acc_empty[i], C::EW * CG);
     }
-    for (int i = 0; i < kEpiWarps; ++i)
-      for (int j = 0; j < 2; ++j) mbar_init(&bar.res[i][j], 1);
+    for (int i = 0; i < C::EW; ++i) mbar_init(&bar.res[i], 1);
     mbar_init(&bar.drain, 1);
     bar.abort = 0;
     fence_barrier_init();
@@ -705,12 +702,12 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = bar.tmem_base;
   const auto aborted = [&] { return *reinterpret_cast<volatile int *>(&bar.abort) != 0; };
-  // B8: the launch gives each of the five warpgroups 96 registers a thread.  The
-  // epilogue needs more (SUM: 128 sums), the others less; the totals are the same:
-  // 64 + 2 * 144 + 2 * 64 = 480, 64 + 2 * 128 + 2 * 80 = 480.
-  if constexpr (C::B8) {
+  // 640 threads: the launch gives each of the five warpgroups 96 registers a thread.
+  // The epilogue needs more (B8 with SUM: 128 sums), the others less; the totals are
+  // the same: 64 + 4 * 104, and with B8 64 + 2 * 144 + 2 * 64 or 64 + 2 * 128 + 2 * 80, 480.
+  if constexpr (C::REGS) {
     if (warp < 4) setmaxnreg_dec<64>();
-    if (warp >= 12) setmaxnreg_dec<C::SUM ? 64 : 80>();
+    if (C::B8 && warp >= 4 + C::EW) setmaxnreg_dec<C::SUM ? 64 : 80>();
   }
 
   if (warp == 0) {
@@ -851,19 +848,19 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
   } else if (warp == 3) {
     if (args.db)
       finish_bias(args.bias_part, args.bias_blocks, args.bias_cols, args.db, args.db_fp32, blockIdx.x, gridDim.x, lane);
-  } else if (warp >= 4 && warp < 4 + kEpiWarps) {
+  } else if (warp >= 4 && warp < 4 + C::EW) {
     // ---------------------------------------------------------------- epilogue
-    if constexpr (C::B8) setmaxnreg_inc<C::SUM ? 144 : 128>();
+    if constexpr (C::REGS) setmaxnreg_inc<!C::B8 ? 104 : C::SUM ? 144 : 128>();
     if constexpr (C::SUM)
       epilogue_sum<C>(mapY, mapZ, args, bar, smem + C::OFF_EPI, tmem, group, (int)rank, warp, lane);
     else
       epilogue_tile<C>(mapY, mapR, mapZ, args, bar, smem + C::OFF_EPI, tmem, group, (int)rank, warp, lane);
-  } else if (C::B8 && warp >= 12) {
+  } else if (C::B8 && warp >= 4 + C::EW) {
     // ---------------------------------------------------------------- converters of the checkpoint operand
     if constexpr (C::B8) {
       // lane -> 16 channels (lane % 8) of token rows cw * ROWS + pass * 4 + lane / 8
       constexpr int ROWS = BK / kConvTeam, PASS = ROWS / 4;
-      const int cw = (warp - 12) % kConvTeam, team = (warp - 12) / kConvTeam;
+      const int cw = (warp - 4 - C::EW) % kConvTeam, team = (warp - 4 - C::EW) / kConvTeam;
       const int unit = lane & 7, sub = lane >> 3;
       const int r0 = cw * ROWS + sub;
       SegIter it(s, group);

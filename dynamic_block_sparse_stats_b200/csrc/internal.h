@@ -96,9 +96,9 @@ cudaError_t make_bf16_map(CUtensorMap *map, const void *base, int rank, const un
                           const unsigned long long *strides, const unsigned *box);
 
 // 2-D tensor map: rows of `cols` elements `ld` elements apart, box box_cols x
-// box_rows; bf16, fp32 and MAP_U8_SW with the 128-byte swizzle (box rows of 128
-// bytes), MAP_U8 without one.
-enum MapType { MAP_BF16, MAP_F32, MAP_U8, MAP_U8_SW };
+// box_rows; bf16 and fp32 with the 128-byte swizzle (box rows of 128 bytes),
+// MAP_U8_SW64 with the 64-byte swizzle (box rows of 64), MAP_U8 without one.
+enum MapType { MAP_BF16, MAP_F32, MAP_U8, MAP_U8_SW64 };
 cudaError_t make_map_2d(CUtensorMap *map, MapType type, const void *base, long long cols, long long rows, long long ld,
                         int box_cols, int box_rows);
 

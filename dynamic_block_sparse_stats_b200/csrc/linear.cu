@@ -37,10 +37,11 @@ using gemm::Sched;
 //   single  128 x 128 tiles, persistent: 0.35 a stage (L2 bound), 4.2 around
 //   split   128 x 64 tiles, the contraction over up to 8 CTAs of a cluster: 0.33
 //           a stage, 5.0 (8 CTAs) to 8.1 (one) around, one tile per cluster
-// An epilogue with an activation, a residual or a saved Z adds 4.0, 1.8 and 0.3
-// behind the last tile.  The least estimate is taken; against all three timed at
-// 27 sizes from 1 x 1024 x 4096 to 92160 x 1024 x 1024, the choice is within a tenth
-// of the best.
+// A wave of tiles takes no less than its epilogues: 1.6 (pairs) and 1.3 (single)
+// us, 2.6 and 2.8 with an activation, a residual or a saved Z ("heavy"), which also
+// adds 2.8, 1.8 and 0.3 behind the last tile.  The least estimate is taken; against
+// all three timed at 27 sizes from 1 x 1024 x 4096 to 92160 x 1024 x 1024, the choice
+// is within a tenth of the best.
 struct Plan {
   int cg, bn;  // tile: 128 * cg rows, bn columns
   int split;   // > 0: split_kernel with clusters of this size
@@ -92,7 +93,8 @@ static Plan make_plan(int rows, int cols, int kc, bool share, int chain, bool ma
     p.bn = big ? 256 : 128;
     p.s = make_sched(p.cg, p.bn, rows, cols, kc, share);
     const double waves = p.s.rem ? (double)p.s.full / p.s.groups : (double)((p.s.tiles + p.s.groups - 1) / p.s.groups);
-    p.us = (big ? 6.0 : 4.2) + (heavy ? (big ? 4.0 : 1.8) : 0.0) + waves * kc * (big ? 0.40 : 0.35);
+    const double epilogue = big ? (heavy ? 2.6 : 1.6) : (heavy ? 2.8 : 1.3);
+    p.us = (big ? 6.0 : 4.2) + (heavy ? (big ? 2.8 : 1.8) : 0.0) + waves * std::max(kc * (big ? 0.40 : 0.35), epilogue);
     // the shared tiles, and the kernel that adds their parts
     if (p.s.rem) p.us += p.s.km * (big ? 0.40 : 0.35) + 5.0 + 0.02 * p.s.groups / p.s.rem;
     if (p.us < best.us) best = p;
@@ -219,12 +221,25 @@ static cudaError_t launch_split(const Plan &p, const Maps &m, const Args &args, 
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+// Whether a pair tile's epilogue gets 16 warps.  Eight are enough once the
+// products of a tile (kc stages) take longer than its epilogue; below that the
+// epilogue sets the time.  Measured at 92160 tokens, 8 against 16 warps (us):
+//   no activation     256 -> 256: 21.3, 18.8   512 -> 512: 44.5, 50.5
+//   bias, residual    512 -> 512: 63, 59       1024 -> 1024: 161, 176
+//   bias, gelu        768 -> 768: 104, 97      1024 -> 1024: 156, 161
+//   and Z saved       768 -> 768: 126, 114     1024 -> 1024: 186, 180
+static bool wide_epilogue(const Args &a) {
+  const int enough = a.save_z ? 48 : a.act == PRISM_ACT_SILU || a.act == PRISM_ACT_GELU ? 14 : a.has_res ? 9 : 6;
+  return a.s.kc < enough;
+}
+
 template <bool A_MN, bool B_MN>
 static cudaError_t launch_plan(const Plan &p, const Maps &m, const Args &args, cudaStream_t st) {
   if (p.split && p.swap) return launch_split<B_MN, A_MN, true>(p, m, args, st);
   if (p.split) return launch_split<A_MN, B_MN>(p, m, args, st);
-  if (p.cg == 2) return launch<Cfg<2, 256, A_MN, B_MN>>(m, args, st);
-  return launch<Cfg<1, 128, A_MN, B_MN>>(m, args, st);
+  if (p.cg == 1) return launch<Cfg<1, 128, A_MN, B_MN>>(m, args, st);
+  if (wide_epilogue(args)) return launch<Cfg<2, 256, A_MN, B_MN, false, false, 16>>(m, args, st);
+  return launch<Cfg<2, 256, A_MN, B_MN>>(m, args, st);
 }
 
 static cudaError_t forward(const prism_linear_t &l, const uint16_t *X, long long ldx, const uint16_t *W,
@@ -264,7 +279,7 @@ static cudaError_t forward(const prism_linear_t &l, const uint16_t *X, long long
     m.r = m.z = m.y;
     if (R && (e = rows_map(&m.r, R, cols, rows, ldr, 32)) != cudaSuccess) return e;
     if (Z && (e = rows_map(&m.z, Z, cols, rows, cols, 32)) != cudaSuccess) return e;
-    if (Z8 && (e = make_map_2d(&m.z, MAP_U8_SW, Z8->codes, Z8->ld, rows, Z8->ld, 128, 32)) != cudaSuccess) return e;
+    if (Z8 && (e = make_map_2d(&m.z, MAP_U8_SW64, Z8->codes, Z8->ld, rows, Z8->ld, 64, 32)) != cudaSuccess) return e;
   }
   return launch_plan<false, false>(p, m, a, st);
 }
