@@ -155,6 +155,39 @@ def test_large(n, cin, cout):
         assert rel(g.db, dz.sum(0)) < rms
 
 
+@pytest.mark.parametrize("n,cin,cout", [(20000, 1024, 1024), (9001, 712, 1000), (9001, 264, 2056), (50, 72, 136)])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_checkpointed_weight_gradient_is_the_restored_ones(n, cin, cout, fp32):
+    """The checkpoint's values are exact in bf16, so converting codes on the way
+    to the tensor cores and restoring the tensor first give the same bits."""
+    d = _inputs(n, cin, cout)
+    x8 = api.ckpt8_pack(d["X"])
+    a = api.linear_bwd(d["dY"], x8, None, need=("dW",), grad_fp32=fp32)
+    b = api.linear_bwd(d["dY"], api.ckpt8_unpack(x8), None, need=("dW",), grad_fp32=fp32)
+    assert torch.equal(a.dW, b.dW)
+
+
+@pytest.mark.parametrize("n,cin,cout", [(20000, 128, 512), (20000, 256, 776), (12000, 520, 1032), (6000, 1024, 2048)])
+def test_epilogues_of_the_pair_tiles(n, cin, cout):
+    """Short contractions take the wide epilogue, long ones the narrow: every
+    combination of what it does, at the rows of the first and last tiles."""
+    d = _inputs(n, cin, cout)
+    rows = torch.cat([torch.arange(300), torch.arange(n - 300, n)]).cuda()
+    part = {k: v[rows].contiguous() if k in ("X", "R") else v for k, v in d.items()}
+    for act in (api.ACT_NONE, api.ACT_RELU, api.ACT_GELU):
+        for bias in (False, True):
+            for res in (False, True):
+                for save in (None, "bf16", "ckpt8"):
+                    f = api.linear_fwd(d["X"], d["W"], d["b"] if bias else None, act, d["R"] if res else None, save)
+                    assert api.workspace_status(f.ws) == 0
+                    z = f.Z
+                    if save == "bf16":
+                        z = f.Z[rows]
+                    elif save == "ckpt8":
+                        z = api.Ckpt8(f.Z.codes[rows].contiguous(), f.Z.scales[rows].contiguous(), cout)
+                    _check_fwd(part, api.LinearResult(f.Y[rows], z, f.ws), act, bias, res)
+
+
 def test_gradients_against_differences():
     """<dY, Y> moved along a direction of X, W or bias, in float64 of the oracle,
     against the kernel's gradient along that direction: a central difference of
