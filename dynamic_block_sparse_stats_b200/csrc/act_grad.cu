@@ -63,13 +63,30 @@ struct Src {
   int *status;
 };
 
+// A checkpointed X that the weight gradient wants restored rides along: the grid's
+// rows from `row` on restore it (one launch less; `row` is the grid's height if
+// there is none).
+struct Restore {
+  int row;
+  const uint2 *codes;
+  const uint8_t *scales;
+  Walk w;
+  int vec;
+  uint4 *x;
+};
+
 // tx threads (a power of two, 8..32) cover 8 * tx columns of a row
 template <int ACT, bool Z8>
 __global__ void __launch_bounds__(kThreads, (Depth<ACT, Z8>::ctas))
-    act_grad_kernel(const Src s, long long n, int vecs, int tx, long long rows_per, float *__restrict__ part) {
+    act_grad_kernel(const Src s, const Restore re, long long n, int vecs, int tx, long long rows_per, float *__restrict__ part) {
   constexpr int ROWS = Depth<ACT, Z8>::rows;
   __shared__ float red[kThreads][9];
   gemm::reset_status(s.status, 1);
+  if ((int)blockIdx.y >= re.row) {
+    const long long cta = (long long)(blockIdx.y - re.row) * gridDim.x + blockIdx.x;
+    unpack_walk<4>(re.codes, re.scales, re.w, re.vec, re.x, re.vec, (cta * kThreads + threadIdx.x) >> 4);
+    return;
+  }
   const int cx = threadIdx.x & (tx - 1), ry = threadIdx.x / tx, rows_step = kThreads / tx;
   const int cv = blockIdx.x * tx + cx;
   const long long r0 = (long long)blockIdx.y * rows_per + ry;
@@ -178,6 +195,7 @@ static Shape shape_of(long long n, int cols) {
 
 struct Launch {
   Src s;
+  Restore re;
   dim3 grid;
   long long n;
   int vecs, tx;
@@ -188,9 +206,9 @@ struct Launch {
 template <int ACT>
 static void run(const Launch &l, bool z8) {
   if (z8)
-    act_grad_kernel<ACT, true><<<l.grid, kThreads, 0, l.st>>>(l.s, l.n, l.vecs, l.tx, l.rows_per, l.part);
+    act_grad_kernel<ACT, true><<<l.grid, kThreads, 0, l.st>>>(l.s, l.re, l.n, l.vecs, l.tx, l.rows_per, l.part);
   else
-    act_grad_kernel<ACT, false><<<l.grid, kThreads, 0, l.st>>>(l.s, l.n, l.vecs, l.tx, l.rows_per, l.part);
+    act_grad_kernel<ACT, false><<<l.grid, kThreads, 0, l.st>>>(l.s, l.re, l.n, l.vecs, l.tx, l.rows_per, l.part);
 }
 
 }  // namespace actg
@@ -201,7 +219,7 @@ size_t act_grad_part_bytes(long long n, int cols) {
 
 cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, long long ldy, const uint16_t *Z,
                             long long ldz, const prism_ckpt8_t *Z8, uint16_t *dZ, float *part, int *status,
-                            cudaStream_t st) {
+                            const prism_ckpt8_t *X8, int width, uint16_t *X, cudaStream_t st) {
   const actg::Shape sh = actg::shape_of(n, cols);
   actg::Src s;
   s.dY = reinterpret_cast<const uint4 *>(dY);
@@ -213,8 +231,22 @@ cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, 
   s.ldq = Z8 ? Z8->ld : 0;
   s.dZ = reinterpret_cast<uint4 *>(dZ);
   s.status = status;
-  const dim3 grid(sh.strips, sh.blocks);
-  const actg::Launch l{s, grid, n, cols / 8, sh.tx, sh.rows_per, part, st};
+  dim3 grid(sh.strips, sh.blocks);
+  actg::Restore re = {};
+  re.row = sh.blocks;
+  if (X8) {
+    // whole grid rows of CTAs, four groups a half-warp or 24 CTAs an SM
+    const long long per_cta = actg::kThreads / 16 * 4, groups = n * (X8->ld / 128);
+    const long long ctas = std::min((groups + per_cta - 1) / per_cta, (long long)device_sm_count() * 24);
+    const long long rows = std::min((ctas + sh.strips - 1) / sh.strips, 65535LL - sh.blocks);
+    grid.y += (unsigned)rows;
+    re.codes = reinterpret_cast<const uint2 *>(X8->codes);
+    re.scales = X8->scales;
+    re.w = make_walk(n, X8->ld, rows * sh.strips * (actg::kThreads / 16));
+    re.vec = width / 8;
+    re.x = reinterpret_cast<uint4 *>(X);
+  }
+  const actg::Launch l{s, re, grid, n, cols / 8, sh.tx, sh.rows_per, part, st};
   switch (act) {
     case PRISM_ACT_RELU:
       actg::run<PRISM_ACT_RELU>(l, Z8 != nullptr);
@@ -227,7 +259,7 @@ cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, 
       break;
     default:
       actg::act_grad_kernel<PRISM_ACT_NONE, false>
-          <<<grid, actg::kThreads, 0, st>>>(s, n, l.vecs, l.tx, l.rows_per, l.part);
+          <<<grid, actg::kThreads, 0, st>>>(s, l.re, n, l.vecs, l.tx, l.rows_per, l.part);
   }
   count_launches(1);
   cudaError_t e = cudaGetLastError();

@@ -24,29 +24,6 @@ constexpr int kThreads = 256;
 // 163.8 -> 153.9; pack with two groups instead of four 144.2, unpack 164.4.
 constexpr int kPackUnroll = 2, kUnpackUnroll = 4, kCtasPerSm = 24;
 
-// Groups 0 .. groups-1, gpr to a row; a half-warp takes every nhalf-th.  Its
-// place (row, group of the row) moves by (row_step, col_step), nhalf divided by gpr.
-struct Walk {
-  long long groups, nhalf, row_step;
-  int gpr, col_step;
-};
-struct Place {
-  long long g, row;
-  int col;
-  __device__ __forceinline__ Place(const Walk &w, long long start) : g(start), row(start / w.gpr) {
-    col = (int)(start - row * w.gpr);
-  }
-  __device__ __forceinline__ void step(const Walk &w) {
-    g += w.nhalf;
-    row += w.row_step;
-    col += w.col_step;
-    if (col >= w.gpr) {
-      col -= w.gpr;
-      ++row;
-    }
-  }
-};
-
 // vec: 16-byte vectors of a row that exist (the rest of the last group is zero)
 __global__ void __launch_bounds__(kThreads)
     pack_kernel(const uint4 *__restrict__ x, long long ld_vec, int vec, const Walk w, uint2 *__restrict__ codes,
@@ -100,44 +77,14 @@ __global__ void __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(kThreads)
     unpack_kernel(const uint2 *__restrict__ codes, const uint8_t *__restrict__ scales, const Walk w, int vec,
                   uint4 *__restrict__ x, long long ld_vec) {
-  const int l16 = threadIdx.x & 15;
-  Place p(w, ((long long)blockIdx.x * kThreads + threadIdx.x) >> 4);
-  while (p.g < w.groups) {
-    uint2 q[kUnpackUnroll];
-    uint32_t s[kUnpackUnroll];
-    uint4 *dst[kUnpackUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnpackUnroll; ++u) {
-      const int c = p.col * 16 + l16;
-      dst[u] = nullptr;
-      if (p.g < w.groups) {
-        q[u] = __ldcs(codes + p.g * 16 + l16);
-        s[u] = __ldcs(scales + p.g * 4 + (l16 >> 2));
-        if (c < vec) dst[u] = x + p.row * ld_vec + c;
-      }
-      p.step(w);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnpackUnroll; ++u) {
-      if (!dst[u]) continue;
-      const uint32_t s2 = ckpt8_scale2(s[u]);
-      __stcs(dst[u], make_uint4(ckpt8_restore2(q[u].x, 0x4140, s2), ckpt8_restore2(q[u].x, 0x4342, s2),
-                                ckpt8_restore2(q[u].y, 0x4140, s2), ckpt8_restore2(q[u].y, 0x4342, s2)));
-    }
-  }
+  unpack_walk<kUnpackUnroll>(codes, scales, w, vec, x, ld_vec, ((long long)blockIdx.x * kThreads + threadIdx.x) >> 4);
 }
 
 // one iteration of `unroll` groups per half-warp, or full occupancy
 Walk walk_for(long long n, long long ld, int unroll, int &grid) {
-  Walk w;
-  w.gpr = (int)(ld / 128);
-  w.groups = n * w.gpr;
   const long long per_cta = (long long)(kThreads / 16) * unroll;
-  grid = (int)std::min<long long>((w.groups + per_cta - 1) / per_cta, (long long)device_sm_count() * kCtasPerSm);
-  w.nhalf = (long long)grid * (kThreads / 16);
-  w.row_step = w.nhalf / w.gpr;
-  w.col_step = (int)(w.nhalf % w.gpr);
-  return w;
+  grid = (int)std::min<long long>((n * (ld / 128) + per_cta - 1) / per_cta, (long long)device_sm_count() * kCtasPerSm);
+  return make_walk(n, ld, (long long)grid * (kThreads / 16));
 }
 
 int check(const char *who, const uint16_t *x, int64_t n, int32_t width, int64_t ld, const prism_ckpt8_t *c) {
@@ -173,7 +120,7 @@ int finish(const char *who, cudaError_t e) {
 cudaError_t launch_ckpt8_unpack(const prism_ckpt8_t &in, long long n, int width, uint16_t *x, long long ld,
                                 cudaStream_t st) {
   int grid;
-  const ck8::Walk w = ck8::walk_for(n, in.ld, ck8::kUnpackUnroll, grid);
+  const Walk w = ck8::walk_for(n, in.ld, ck8::kUnpackUnroll, grid);
   ck8::unpack_kernel<<<grid, ck8::kThreads, 0, st>>>(reinterpret_cast<const uint2 *>(in.codes), in.scales, w, width / 8,
                                                      reinterpret_cast<uint4 *>(x), ld / 8);
   count_launches(1);
@@ -195,7 +142,7 @@ extern "C" int prism_ckpt8_pack(const uint16_t *x, int64_t n, int32_t width, int
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int grid;
-  const ck8::Walk w = ck8::walk_for(n, out->ld, ck8::kPackUnroll, grid);
+  const Walk w = ck8::walk_for(n, out->ld, ck8::kPackUnroll, grid);
   ck8::pack_kernel<<<grid, ck8::kThreads, 0, st>>>(reinterpret_cast<const uint4 *>(x), (long long)(ld / 8), width / 8, w,
                                                    reinterpret_cast<uint2 *>(out->codes),
                                                    reinterpret_cast<uint32_t *>(out->scales));

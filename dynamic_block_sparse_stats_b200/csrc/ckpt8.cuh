@@ -99,4 +99,70 @@ __device__ __forceinline__ void ckpt8_restore16(const uint4 &q, uint32_t s, uint
                   ckpt8_restore2(q.w, 0x4342, s2));
 }
 
+// Groups 0 .. groups-1, gpr to a row; a half-warp takes every nhalf-th.  Its
+// place (row, group of the row) moves by (row_step, col_step), nhalf divided by gpr.
+struct Walk {
+  long long groups, nhalf, row_step;
+  int gpr, col_step;
+};
+struct Place {
+  long long g, row;
+  int col;
+  __device__ __forceinline__ Place(const Walk &w, long long start) : g(start), row(start / w.gpr) {
+    col = (int)(start - row * w.gpr);
+  }
+  __device__ __forceinline__ void step(const Walk &w) {
+    g += w.nhalf;
+    row += w.row_step;
+    col += w.col_step;
+    if (col >= w.gpr) {
+      col -= w.gpr;
+      ++row;
+    }
+  }
+};
+
+inline Walk make_walk(long long n, long long ld, long long nhalf) {
+  Walk w;
+  w.gpr = (int)(ld / 128);
+  w.groups = n * w.gpr;
+  w.nhalf = nhalf;
+  w.row_step = nhalf / w.gpr;
+  w.col_step = (int)(nhalf % w.gpr);
+  return w;
+}
+
+// The half-warp `half` of `w.nhalf` restores its groups, UNROLL at a time; vec:
+// 16-byte vectors of a row that exist.
+template <int UNROLL>
+__device__ __forceinline__ void unpack_walk(const uint2 *__restrict__ codes, const uint8_t *__restrict__ scales,
+                                            const Walk &w, int vec, uint4 *__restrict__ x, long long ld_vec,
+                                            long long half) {
+  const int l16 = threadIdx.x & 15;
+  Place p(w, half);
+  while (p.g < w.groups) {
+    uint2 q[UNROLL];
+    uint32_t s[UNROLL];
+    uint4 *dst[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const int c = p.col * 16 + l16;
+      dst[u] = nullptr;
+      if (p.g < w.groups) {
+        q[u] = __ldcs(codes + p.g * 16 + l16);
+        s[u] = __ldcs(scales + p.g * 4 + (l16 >> 2));
+        if (c < vec) dst[u] = x + p.row * ld_vec + c;
+      }
+      p.step(w);
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      if (!dst[u]) continue;
+      const uint32_t s2 = ckpt8_scale2(s[u]);
+      __stcs(dst[u], make_uint4(ckpt8_restore2(q[u].x, 0x4140, s2), ckpt8_restore2(q[u].x, 0x4342, s2),
+                                ckpt8_restore2(q[u].y, 0x4140, s2), ckpt8_restore2(q[u].y, 0x4342, s2)));
+    }
+  }
+}
+
 }  // namespace prism

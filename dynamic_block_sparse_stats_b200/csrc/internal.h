@@ -104,12 +104,13 @@ cudaError_t make_map_2d(CUtensorMap *map, MapType type, const void *base, long l
 
 // act_grad.cu: dZ = dY act'(Z) (nothing to write without an activation) and, with
 // `part` (act_grad_part_bytes), act_grad_blocks rows of partial column sums of
-// dZ; clears the status word.  launch_bias_grad adds the rows up into db.
+// dZ; clears the status word; restores X8 (NULL: nothing) into X [n][width].
+// launch_bias_grad adds the rows up into db.
 size_t act_grad_part_bytes(long long n, int cols);
 int act_grad_blocks(long long n, int cols);
 cudaError_t launch_act_grad(long long n, int cols, int act, const uint16_t *dY, long long ldy, const uint16_t *Z,
                             long long ldz, const prism_ckpt8_t *Z8, uint16_t *dZ, float *part, int *status,
-                            cudaStream_t st);
+                            const prism_ckpt8_t *X8, int width, uint16_t *X, cudaStream_t st);
 cudaError_t launch_bias_grad(long long n, int cols, const float *part, void *db, int db_fp32, cudaStream_t st);
 
 // ckpt8.cu: x[n][ld] = the values of a checkpoint
