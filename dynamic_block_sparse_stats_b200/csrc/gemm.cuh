@@ -1134,6 +1134,18 @@ __global__ void __launch_bounds__(256, 2)
       *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(args.Y) + (long long)m * args.ldy + c) =
           make_uint2(pack_bf16(lo.x, lo.y), pack_bf16(hi.x, hi.y));
     }
+    // Rows of codes are padded to 128 channels, 64-column tiles to 64: where that leaves
+    // half a group behind the last tile, it is part of the checkpoint too (codes 0).
+    const int past = n0 + 64;
+    if (!SWAP && args.save_z == 2 && past == args.s.tiles_n * 64 && past < args.ldq) {
+      for (int x = rank * 256 + threadIdx.x; x < 512; x += 256 * split) {
+        const int m = m0 + (x >> 2);
+        if (m >= args.rows) break;
+        *reinterpret_cast<uint4 *>(args.codes + (long long)m * args.ldq + past + (x & 3) * 16) = make_uint4(0, 0, 0, 0);
+        if ((x & 3) == 0)
+          *reinterpret_cast<uint16_t *>(args.scales + (long long)m * (args.ldq / 32) + past / 32) = 0x0101;
+      }
+    }
   }
   cluster_sync_all();  // no CTA leaves while another reads its partial tile
 }

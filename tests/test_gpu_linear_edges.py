@@ -1,0 +1,50 @@
+"""What lies at the edges of the linear map's calls: the padding of a saved
+checkpoint and the buffers around it."""
+import pytest
+import torch
+
+from dynamic_block_sparse_stats_b200 import api
+
+pytestmark = pytest.mark.gpu
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _rand(g, *shape, s=1.0):
+    return (s * torch.randn(*shape, generator=g, device="cuda")).to(torch.bfloat16)
+
+
+def _framed(n, width, byte):
+    """A checkpoint filled with `byte`, between two more rows of it."""
+    ld = (width + 127) // 128 * 128
+    codes = torch.full((n + 2, ld), byte, dtype=torch.uint8, device="cuda").view(torch.int8)
+    scales = torch.full((n + 2, ld // 32), byte, dtype=torch.uint8, device="cuda")
+    return codes, scales, api.Ckpt8(codes[1:n + 1], scales[1:n + 1], width)
+
+
+# `out` ends 8..64 channels past a multiple of 128 (and elsewhere), at sizes of
+# every kernel: few tokens, the split contraction, single and pair tiles
+@pytest.mark.parametrize("n,cin,cout", [(129, 264, 320), (300, 64, 1288), (512, 1024, 192), (2049, 192, 192), (200, 1024, 64),
+                                        (65, 64, 8), (77, 520, 136), (1, 64, 8), (16, 512, 136), (33, 1000, 40),
+                                        (129, 264, 328), (1003, 328, 712), (5000, 264, 1288), (20000, 256, 776),
+                                        (20000, 1024, 1032)])
+def test_a_saved_checkpoint_is_written_whole(n, cin, cout):
+    """Codes at channels past `out` are 0 whatever the buffer held, the blocks that
+    exist are the same, and nothing is written outside the rows."""
+    g = _gen(n + cout)
+    X, W, b = _rand(g, n, cin), _rand(g, cout, cin, s=cin ** -0.5), _rand(g, cout)
+    seen = []
+    for byte in (0x55, 0xAA):
+        codes, scales, z = _framed(n, cout, byte)
+        f = api.linear_fwd(X, W, b, api.ACT_GELU, save="ckpt8", Z=z)
+        assert api.workspace_status(f.ws) == 0 and f.Z is z
+        assert (z.codes[:, cout:] == 0).all()
+        for frame in (codes.view(torch.uint8), scales):
+            assert (frame[0] == byte).all() and (frame[-1] == byte).all()
+        seen.append((z.codes, z.scales))
+    assert torch.equal(seen[0][0], seen[1][0]) and torch.equal(seen[0][1], seen[1][1])
+    assert torch.equal(api.ckpt8_unpack(z), api.ckpt8_unpack(api.linear_fwd(X, W, b, api.ACT_GELU, save="ckpt8").Z))
