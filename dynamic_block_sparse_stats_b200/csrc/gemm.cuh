@@ -1064,7 +1064,7 @@ __global__ void __launch_bounds__(256, 2)
   cluster_sync_all();
   tc_fence_after();
   if (warp == 2) tmem_dealloc_g<1>(tmem, 64);
-  if (!*reinterpret_cast<volatile int *>(&bar.abort)) {
+  if (!__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&bar.abort))) {
     constexpr int UNITS = SWAP ? 32 : 16;  // four-column pieces of a row
     const int om = SWAP ? n0 : m0, on = SWAP ? m0 : n0;  // the tile's place in the output
 #pragma unroll 1
@@ -1147,6 +1147,9 @@ __global__ void __launch_bounds__(256, 2)
       }
     }
   }
+  // Lanes outside the output have left the loop's body early; the aligned barrier wants
+  // the whole warp at once.
+  __syncwarp();
   cluster_sync_all();  // no CTA leaves while another reads its partial tile
 }
 

@@ -48,3 +48,23 @@ def test_a_saved_checkpoint_is_written_whole(n, cin, cout):
         seen.append((z.codes, z.scales))
     assert torch.equal(seen[0][0], seen[1][0]) and torch.equal(seen[0][1], seen[1][1])
     assert torch.equal(api.ckpt8_unpack(z), api.ckpt8_unpack(api.linear_fwd(X, W, b, api.ACT_GELU, save="ckpt8").Z))
+
+
+@pytest.mark.parametrize("cin,cout", [(8, 8), (40, 72), (72, 136), (200, 200)])
+def test_ragged_tiles_of_the_split_kernel_again_and_again(cin, cout):
+    """Outputs that end inside a tile, in rows and columns: lanes with nothing to
+    store meet the others at the kernel's last barrier, call after call."""
+    g = _gen(cin)
+    n = 1500
+    X, W, dY = _rand(g, n, cin), _rand(g, cout, cin), _rand(g, n, cout)
+    first = None
+    for _ in range(40):
+        f = api.linear_fwd(X[:131], W, save="ckpt8")
+        b = api.linear_bwd(dY, X, W, grad_fp32=True)
+        got = (f.Y, f.Z.codes, b.dX, b.dW, b.db)
+        first = first or got
+        assert api.workspace_status(f.ws) == 0 and api.workspace_status(b.ws) == 0
+        assert all(torch.equal(u, v) for u, v in zip(first, got))
+    # exact products, n additions of at most 2^-23 of the running magnitude each
+    a, x = dY.double().t(), X.double()
+    assert ((first[3] - a @ x).abs() <= n * 2.0 ** -23 * (a.abs() @ x.abs())).all()
