@@ -562,7 +562,8 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
     """prism_linear_fwd: Y = act(X W^T + bias) + residual.  X bf16 [n, in], W
     bf16 [out, in], bias bf16 [out], residual bf16 [n, out]; X, residual and Y
     rows may be strided.  save = "bf16" or "ckpt8" keeps the pre-activation for
-    linear_bwd (into Z when given)."""
+    linear_bwd (into Z when given).  Y may be the residual itself; otherwise the
+    library refuses outputs that share memory with an input or one another."""
     ldx = _check_rows(X, "X")
     n, cin = X.shape
     if not isinstance(W, torch.Tensor) or W.dim() != 2:
@@ -614,8 +615,9 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
     bf16 [n, out], the forward's X [n, in] (bf16 or a Ckpt8; needed for dW), W
     (needed for dX) and, with an activation, the saved pre-activation Z (bf16 or
     a Ckpt8).  dX is bf16; dW and db bf16, or fp32 with grad_fp32.  `out` may
-    hold (dX, dW, db) buffers, None entries allocated.  The residual's gradient
-    is dY itself."""
+    hold (dX, dW, db) buffers, None entries allocated; the library refuses
+    buffers that share memory with what the call reads (X's for dX unless `need`
+    leaves dW out) or with one another.  The residual's gradient is dY itself."""
     lddy = _check_rows(dY, "dY")
     n, cout = dY.shape
     want_x, want_w, want_b = "dX" in need, "dW" in need, "db" in need

@@ -94,6 +94,25 @@ int check_plan_call(const prism_params *p, const uint16_t *V, const float *a2v_n
   return check_plan(out);
 }
 
+// whether a row of `m` meets the bytes [lo, hi), which lie within its range of addresses at least in part
+static bool row_in(const Span &m, uint64_t lo, uint64_t hi) {
+  if (lo < m.at || m.rows == 1) return true;
+  const uint64_t i = (lo - m.at) / m.pitch;
+  if (i < m.rows && lo - m.at - i * m.pitch < m.bytes) return true;
+  return i + 1 < m.rows && m.at + (i + 1) * m.pitch < hi;
+}
+
+bool overlap(const Span &a, const Span &b) {
+  if (a.empty() || b.empty() || a.end() <= b.at || b.end() <= a.at) return false;
+  if (a.rows == 1) return row_in(b, a.at, a.end());
+  if (b.rows == 1) return row_in(a, b.at, b.end());
+  if (a.pitch != b.pitch) return true;
+  const Span &u = a.at <= b.at ? a : b, &v = a.at <= b.at ? b : a;
+  // v's first row begins r bytes into the pitch of u's row q; its later rows, as far into the later ones
+  const uint64_t q = (v.at - u.at) / u.pitch, r = (v.at - u.at) % u.pitch;
+  return (q < u.rows && r < u.bytes) || (q + 1 < u.rows && r + v.bytes > u.pitch);
+}
+
 int report_error(int code, const char *msg) { return fail(code, "%s", msg); }
 
 void clear_error() { g_last_error.clear(); }

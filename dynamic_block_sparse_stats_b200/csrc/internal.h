@@ -120,6 +120,31 @@ cudaError_t launch_ckpt8_unpack(const prism_ckpt8_t &in, long long n, int width,
 // SMs of the current device (148 where there is none)
 int device_sm_count();
 
+// A matrix in device memory as addresses: `rows` rows of `bytes` bytes, `pitch` apart.
+struct Span {
+  const char *name;
+  uint64_t at;
+  uint64_t rows, bytes, pitch;
+  Span(const char *name_, const void *p, uint64_t rows_, uint64_t bytes_, uint64_t pitch_ = 0)
+      : name(name_), at(reinterpret_cast<uint64_t>(p)), rows(p ? rows_ : 0), bytes(bytes_), pitch(pitch_) {
+    if (rows > 1 && pitch == bytes) {  // no gaps: one row
+      bytes *= rows;
+      rows = 1;
+    }
+  }
+  bool empty() const { return rows == 0 || bytes == 0; }
+  // one past the last byte (held at the top: a row stride of a one-token call may be anything)
+  uint64_t end() const {
+    const uint64_t last = rows > 1 ? rows - 1 : 0;
+    if (last && pitch > (UINT64_MAX - at - bytes) / last) return UINT64_MAX;
+    return at + last * pitch + bytes;
+  }
+};
+// Whether two of them share a byte: exact where one has no gaps or the strides agree
+// (column slices of one buffer do not overlap); where two strides differ, by the
+// ranges of addresses.
+bool overlap(const Span &a, const Span &b);
+
 // host-side count of kernel launches (prism_kernel_launches)
 void count_launches(int n);
 

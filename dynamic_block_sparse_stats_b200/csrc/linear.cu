@@ -467,6 +467,26 @@ static int check_workspace(void *ws, size_t bytes, size_t need) {
   return PRISM_OK;
 }
 
+// The rules on shared memory: no output on anything that the call reads (but Y in
+// place of its residual, where each thread reads what it overwrites), no two outputs
+// on one another.
+template <size_t O, size_t I>
+static int check_apart(const Span (&out)[O], const Span (&in)[I], const Span *in_place = nullptr) {
+  for (size_t o = 0; o < O; ++o) {
+    for (size_t i = 0; i < I; ++i)
+      if (!(o == 0 && &in[i] == in_place) && overlap(out[o], in[i]))
+        return refuse(PRISM_ERR_INVALID_ARG, "linear: %s overlaps %s", out[o].name, in[i].name);
+    for (size_t k = 0; k < o; ++k)
+      if (overlap(out[o], out[k]))
+        return refuse(PRISM_ERR_INVALID_ARG, "linear: %s overlaps %s", out[o].name, out[k].name);
+  }
+  return PRISM_OK;
+}
+static Span rows_span(const char *name, const void *p, long long rows, int cols, long long ld) {
+  return Span(name, p, rows, 2 * (uint64_t)cols, 2 * (uint64_t)ld);
+}
+static Span flat_span(const char *name, const void *p, uint64_t bytes) { return Span(name, p, 1, bytes); }
+
 // workspace of the backward: header, dZ (with an activation), the bias
 // gradient's partial sums, the weight gradient's, X where it is restored
 struct BwdWs {
@@ -522,6 +542,16 @@ int prism_linear_fwd(const prism_linear_t *l, const uint16_t *X, int64_t ldx, co
     return rc;
   if (Z8 && l->n > 0 && (rc = check_ckpt("Z8", Z8, l->out)) != PRISM_OK) return rc;
   if ((rc = check_workspace(workspace, ws_bytes, kWsHeader)) != PRISM_OK) return rc;
+  {
+    const long long n = l->n, ldq = Z8 ? Z8->ld : 0;
+    const Span out[] = {rows_span("Y", Y, n, l->out, ldy), rows_span("Z", Z, n, l->out, l->out),
+                        flat_span("Z8 (codes)", Z8 ? Z8->codes : nullptr, n * ldq),
+                        flat_span("Z8 (scales)", Z8 ? Z8->scales : nullptr, n * ldq / 32),
+                        flat_span("the workspace", workspace, kWsHeader)};
+    const Span in[] = {rows_span("R", R, n, l->out, ldr), rows_span("X", X, n, l->in, ldx),
+                       rows_span("W", W, l->out, l->in, l->in), flat_span("bias", bias, 2 * (uint64_t)l->out)};
+    if ((rc = check_apart(out, in, R == Y && (ldr == ldy || n == 1) ? &in[0] : nullptr)) != PRISM_OK) return rc;
+  }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (l->n == 0)
@@ -559,6 +589,20 @@ int prism_linear_bwd(const prism_linear_t *l, const uint16_t *dY, int64_t lddy, 
     return rc;
   const BwdWs b = carve_bwd(*l, X8 != nullptr, workspace);
   if ((rc = check_workspace(workspace, ws_bytes, b.bytes)) != PRISM_OK) return rc;
+  {
+    // what is read: X only for dW, W only for dX, Z only with an activation
+    const long long n = l->n;
+    const uint64_t elem = grad_fp32 ? 4 : 2;
+    const prism_ckpt8_t none = {}, &x8 = X8 && dW ? *X8 : none, &z8 = Z8 && act ? *Z8 : none;
+    const Span out[] = {rows_span("dX", dX, n, l->in, l->in), flat_span("dW", dW, elem * l->in * l->out),
+                        flat_span("db", db, elem * l->out), flat_span("the workspace", workspace, b.bytes)};
+    const Span in[] = {rows_span("dY", dY, n, l->out, lddy), rows_span("X", dW ? X : nullptr, n, l->in, ldx),
+                       flat_span("X8 (codes)", x8.codes, n * x8.ld), flat_span("X8 (scales)", x8.scales, n * x8.ld / 32),
+                       rows_span("W", dX ? W : nullptr, l->out, l->in, l->in),
+                       rows_span("Z", act ? Z : nullptr, n, l->out, ldz), flat_span("Z8 (codes)", z8.codes, n * z8.ld),
+                       flat_span("Z8 (scales)", z8.scales, n * z8.ld / 32)};
+    if ((rc = check_apart(out, in)) != PRISM_OK) return rc;
+  }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   const size_t elem = grad_fp32 ? 4 : 2;

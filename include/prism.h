@@ -442,7 +442,11 @@ size_t prism_linear_workspace_size(const prism_linear_t *l, int backward);
  *   Z8     the same as a checkpoint, or NULL: quantised from the fp32
  *          pre-activation.  Not together with Z.
  * ldx, ldr, ldy are row strides in elements, multiples of 8.  All pointers are
- * 16-byte aligned.  Other than R = Y, outputs may overlap no input.
+ * 16-byte aligned.  Other than R = Y, no output (Y, Z, Z8, the workspace) may
+ * share memory with an input or another output; calls that would are refused.
+ * Column slices of one buffer, with one row stride, share none; where two
+ * strides differ and neither matrix is contiguous, it goes by the ranges of
+ * addresses.
  * Products are accumulated in fp32; bias, activation and residual are applied
  * in fp32, and Y (and Z) rounded to bf16 once.
  * Returns PRISM_OK, PRISM_ERR_INVALID_ARG, PRISM_ERR_UNSUPPORTED (n * in or
@@ -473,6 +477,10 @@ int prism_linear_fwd(const prism_linear_t *l, const uint16_t *X, int64_t ldx,
  * cores, and of dY itself); db sums the fp32 values.  Every sum is held in
  * fp32 and taken in a fixed order: the outputs are bitwise reproducible.
  * With n = 0, dW and db are zero.
+ * No output (dX, dW, db, the workspace) may share memory with what the call
+ * reads (dY; X or X8 if dW is asked for; W if dX is; Z or Z8 with an
+ * activation) or with another output; calls that would are refused, by the
+ * rule of prism_linear_fwd.  dX may take X's place where dW is not asked for.
  * Returns as prism_linear_fwd.
  */
 int prism_linear_bwd(const prism_linear_t *l, const uint16_t *dY, int64_t lddy,

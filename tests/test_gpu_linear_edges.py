@@ -3,7 +3,7 @@ checkpoint and the buffers around it."""
 import pytest
 import torch
 
-from dynamic_block_sparse_stats_b200 import api
+from dynamic_block_sparse_stats_b200 import _lib, api
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,39 @@ def test_ragged_tiles_of_the_split_kernel_again_and_again(cin, cout):
     # exact products, n additions of at most 2^-23 of the running magnitude each
     a, x = dY.double().t(), X.double()
     assert ((first[3] - a @ x).abs() <= n * 2.0 ** -23 * (a.abs() @ x.abs())).all()
+
+
+def test_an_output_on_an_operand_is_refused_and_changes_nothing():
+    """The input's buffer as dX's, with dW asked for: dW would read dX as X."""
+    n, c = 300, 128
+    g = _gen(3)
+    X, W, dY, Z = _rand(g, n, c), _rand(g, c, c), _rand(g, n, c), _rand(g, n, c)
+    kept = X.clone()
+    for call in (lambda: api.linear_bwd(dY, X, W, out=(X, None, None)),
+                 lambda: api.linear_bwd(dY, X, W, Z, api.ACT_GELU, out=(Z, None, None)),
+                 lambda: api.linear_bwd(dY, X, W, out=(None, W, None)),
+                 lambda: api.linear_fwd(X, W, save="bf16", Z=X),
+                 lambda: api.linear_fwd(X[:c], W, Y=W),
+                 lambda: api.linear_fwd(X[1:], W, residual=X[1:], Y=X[:-1])):
+        with pytest.raises(_lib.PrismError, match="overlaps"):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(X, kept)
+
+
+def test_outputs_beside_operands_in_one_buffer():
+    """Column slices of one buffer share no memory; X's place is free for dX where
+    dW is not asked for; a residual is added in place in a slice."""
+    n, cin, cout = 700, 136, 264
+    g = _gen(4)
+    X, W, b, R, dY = _rand(g, n, cin), _rand(g, cout, cin), _rand(g, cout), _rand(g, n, cout), _rand(g, n, cout)
+    want = api.linear_fwd(X, W, b, api.ACT_SILU, R).Y
+    room = torch.zeros(n, cin + cout + 8, dtype=torch.bfloat16, device="cuda")
+    room[:, :cin], room[:, cin:cin + cout] = X, R
+    x, y = room[:, :cin], room[:, cin:cin + cout]
+    assert torch.equal(api.linear_fwd(x, W, b, api.ACT_SILU, y, Y=y).Y, want)
+    assert torch.equal(x, X) and (room[:, cin + cout:] == 0).all()
+    grads = api.linear_bwd(dY, X, W)
+    place = X.clone()
+    got = api.linear_bwd(dY, place, W, need=("dX", "db"), out=(place, None, None))
+    assert got.dX is place and torch.equal(place, grads.dX) and torch.equal(got.db, grads.db)
