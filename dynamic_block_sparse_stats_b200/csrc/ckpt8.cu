@@ -100,6 +100,12 @@ int check(const char *who, const uint16_t *x, int64_t n, int32_t width, int64_t 
   else if (reinterpret_cast<uintptr_t>(x) % 16 || reinterpret_cast<uintptr_t>(c->codes) % 16 ||
            reinterpret_cast<uintptr_t>(c->scales) % 4)
     bad = "the activation and the codes must be 16-byte aligned, the scales 4-byte";
+  if (!bad) {
+    const Span codes("the codes", c->codes, 1, n * c->ld), scales("the scales", c->scales, 1, n * c->ld / 32);
+    const Span v("the activation", x, n, 2 * (uint64_t)width, 2 * (uint64_t)ld);
+    if (overlap(v, codes) || overlap(v, scales)) bad = "the activation overlaps the checkpoint";
+    else if (overlap(codes, scales)) bad = "the codes overlap the scales";
+  }
   if (!bad) return PRISM_OK;
   snprintf(msg, sizeof(msg), "%s: %s", who, bad);
   return report_error(PRISM_ERR_INVALID_ARG, msg);

@@ -402,6 +402,7 @@ typedef struct prism_ckpt8_t {
  *   out       arrays to fill (host struct of device pointers).
  * prism_ckpt8_unpack -- the activation back: x[n][ld] = code * scale; elements
  * of x at index >= width of a row are left as they were.
+ * x, codes and scales may share no memory; calls where they would are refused.
  * Return PRISM_OK, PRISM_ERR_INVALID_ARG or PRISM_ERR_CUDA.
  */
 int prism_ckpt8_pack(const uint16_t *x, int64_t n, int32_t width, int64_t ld,

@@ -96,3 +96,23 @@ def _bwd(n=N, act=3, dY=_at(0), X=_at(1), X8=None, W=_at(2), Z=_at(3), Z8=None, 
 ])
 def test_backward(kw, names):
     _said(_bwd(**kw), *names)
+
+
+def _pack(x=_at(0), n=N, ld=IN, c=None):
+    return _lib.load().prism_ckpt8_pack(x, n, IN, ld, c or _ck(1), None)
+
+
+def _unpack(x=_at(0), n=N, ld=IN, c=None):
+    return _lib.load().prism_ckpt8_unpack(c or _ck(1), n, IN, x, ld, None)
+
+
+@pytest.mark.parametrize("call", [_pack, _unpack])
+@pytest.mark.parametrize("kw", [dict(x=_at(1)), dict(x=_at(1, BIG // 2)), dict(x=_at(1, 2048 - 16)), dict(x=_at(1, -4096 + 16)),
+                                dict(x=_at(1, -512 * 8), ld=256), dict(x=_at(1, 2048 - 16), n=1 << 12, ld=1 << 20)])
+def test_checkpoints(call, kw):
+    _said(call(**kw), "ckpt8")
+
+
+@pytest.mark.parametrize("call", [_pack, _unpack])
+def test_codes_on_their_scales(call):
+    _said(call(c=C.byref(_lib.PrismCkpt8(2 * BIG, 2 * BIG + 1024, OUT))), "ckpt8")
