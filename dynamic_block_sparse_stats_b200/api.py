@@ -4,6 +4,12 @@ PyTorch provides device memory and the current stream; every computation runs
 in libprism.so.  Tensors follow the layout of include/prism.h:
 Q, K, V, O, dO bf16 [N, heads, head_dim] contiguous on one CUDA device, the
 A2V norm map fp32 [N].
+
+Calls take a torch.cuda.Stream as `stream` (default: the current one).  The
+caller orders it behind whatever made the inputs, and keeps the inputs until it
+is done.  What the call allocates, its workspace included, is that stream's
+memory, and is not given out again before the current stream is done with it
+too.
 """
 from __future__ import annotations
 
@@ -41,6 +47,31 @@ def params_for(w, **over) -> PrismParams:
 def _stream(stream, device) -> int:
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return s.cuda_stream
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _alloc_on(stream, dev):
+    """Where a call's new tensors come from: with an explicit stream, from that
+    stream's memory.  Memory of the current stream may still be in use there when
+    the other stream writes it, and is given out again while that stream runs."""
+    if not isinstance(stream, torch.cuda.Stream):
+        return _HERE
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _hand_over(stream, dev, *made):
+    """New outputs of a call with an explicit stream: their memory waits for the
+    caller's current stream too before it is given out again."""
+    if isinstance(stream, torch.cuda.Stream):
+        here = torch.cuda.current_stream(dev)
+        if here != stream:
+            for t in made:
+                if t is not None:
+                    t.record_stream(here)
 
 
 def _ptr(t):
@@ -115,9 +146,11 @@ def a2v_norm(hhat: torch.Tensor, out: torch.Tensor | None = None, stream=None) -
         _check_tensor(out, "a2v_norm", torch.float32, (n,))
     dev = _check_devices([("hhat", hhat), ("a2v_norm", out)])
     ld = hhat.stride(0) if n > 1 else width
-    with torch.cuda.device(dev):
+    made = out is None
+    with torch.cuda.device(dev), _alloc_on(stream, dev):
         out = out if out is not None else torch.empty((n,), dtype=torch.float32, device=dev)
         check(_lib.load().prism_a2v_norm(_ptr(hhat), n, width, ld, _ptr(out), _stream(stream, dev)))
+    _hand_over(stream, dev, out if made else None)
     return out
 
 
@@ -139,6 +172,9 @@ class Plan:
     perm: torch.Tensor
     inv_perm: torch.Tensor
     ws: torch.Tensor
+
+    def tensors(self):
+        return (self.zone_shape, self.zone_g, self.zone_rho, self.n_blocks, self.blocks, self.perm, self.inv_perm, self.ws)
 
     def c_struct(self) -> PrismPlan:
         return PrismPlan(self.zone_shape.data_ptr(), self.zone_g.data_ptr(), self.zone_rho.data_ptr(),
@@ -187,11 +223,13 @@ def plan(p: PrismParams, V: torch.Tensor, a: torch.Tensor | None = None, out: Pl
         _check_tensor(a, "a2v_norm", torch.float32, (N,))
     named = [("V", V), ("a2v_norm", a)] + (_check_plan(p, out) if out is not None else [])
     dev = _check_devices(named)
-    with torch.cuda.device(dev):
+    made = out is None
+    with torch.cuda.device(dev), _alloc_on(stream, dev):
         out = out if out is not None else alloc_plan(p, dev)
         cs = out.c_struct()
         check(_lib.load().prism_plan(C.byref(p), _ptr(V), _ptr(a), C.byref(cs), _ptr(out.ws), out.ws.numel(),
                                      _stream(stream, dev)))
+    _hand_over(stream, dev, *(out.tensors() if made else ()))
     return out
 
 
@@ -212,12 +250,14 @@ def project_v_plan(p: PrismParams, X: torch.Tensor, Wv: torch.Tensor, a: torch.T
         _check_tensor(a, "a2v_norm", torch.float32, (N,))
     named = [("X", X), ("Wv", Wv), ("V", V), ("a2v_norm", a)] + (_check_plan(p, out) if out is not None else [])
     dev = _check_devices(named)
-    with torch.cuda.device(dev):
+    made_v, made = V is None, out is None
+    with torch.cuda.device(dev), _alloc_on(stream, dev):
         V = V if V is not None else torch.empty((N, p.heads, p.head_dim), dtype=torch.bfloat16, device=dev)
         out = out if out is not None else alloc_plan(p, dev)
         cs = out.c_struct()
         check(_lib.load().prism_project_v_plan(C.byref(p), _ptr(X), Cin, _ptr(Wv), _ptr(V), _ptr(a), C.byref(cs),
                                                _ptr(out.ws), out.ws.numel(), _stream(stream, dev)))
+    _hand_over(stream, dev, V if made_v else None, *(out.tensors() if made else ()))
     return V, out
 
 
@@ -235,6 +275,9 @@ class Selection:
     row: torch.Tensor | None
     nnz: int
     ws: torch.Tensor
+
+    def tensors(self):
+        return (self.row_ptr, self.col, self.col_ptr, self.row, self.ws)
 
     def c_struct(self) -> PrismSelect:
         return PrismSelect(self.row_ptr.data_ptr(), self.col.data_ptr(), self.col.numel(), self.nnz,
@@ -299,7 +342,8 @@ def select(p: PrismParams, pl: Plan, Q: torch.Tensor, K: torch.Tensor, out: Sele
         named += _check_selection(p, out, False)
     dev = _check_devices(named)
     lib = _lib.load()
-    with torch.cuda.device(dev):
+    made, made_col = out is None, False
+    with torch.cuda.device(dev), _alloc_on(stream, dev):
         if out is None:
             out = alloc_select(p, dev, cap if cap is not None else default_capacity(p), transpose)
         cpl = pl.c_struct()
@@ -309,14 +353,16 @@ def select(p: PrismParams, pl: Plan, Q: torch.Tensor, K: torch.Tensor, out: Sele
                                   out.ws.numel(), _stream(stream, dev))
             if rc == _lib.PRISM_ERR_CAPACITY and attempt == 0 and out.col.numel() < cs.nnz <= 0x7fffffff:
                 need = int(cs.nnz)
+                made_col = True
                 out.col = torch.empty((need,), dtype=torch.int32, device=dev)
                 if out.row is not None:
                     out.row = torch.empty((need,), dtype=torch.int32, device=dev)
                 continue
             check(rc)
-            out.nnz = int(cs.nnz)
-            return out
-    raise AssertionError("unreachable")
+            break
+    out.nnz = int(cs.nnz)
+    _hand_over(stream, dev, *(out.tensors() if made else (out.col, out.row) if made_col else ()))
+    return out
 
 
 @dataclass
@@ -352,7 +398,8 @@ def attn_fwd(p: PrismParams, pl: Plan, sel: Selection, Q, K, V, O=None, lse=None
              ("ws", ws)] + _check_plan(p, pl) + _check_selection(p, sel, False)
     dev = _check_devices(named)
     lib = _lib.load()
-    with torch.cuda.device(dev):
+    given = (O, O_res, lse, ws)
+    with torch.cuda.device(dev), _alloc_on(stream, dev):
         O = O if O is not None else torch.empty_like(Q)
         if residual and O_res is None:
             O_res = torch.empty_like(Q)
@@ -362,6 +409,7 @@ def attn_fwd(p: PrismParams, pl: Plan, sel: Selection, Q, K, V, O=None, lse=None
         check(lib.prism_attn_fwd(C.byref(p), C.byref(cpl), C.byref(cs), _ptr(Q), _ptr(K), _ptr(V), _ptr(O),
                                  _ptr(O_res) if residual else None, _ptr(lse), _ptr(ws), ws.numel(),
                                  _stream(stream, dev)))
+    _hand_over(stream, dev, *(t for g, t in zip(given, (O, O_res, lse, ws)) if g is None))
     return FwdResult(O, lse, ws, O_res if residual else None)
 
 
@@ -393,7 +441,8 @@ def attn_bwd(p: PrismParams, pl: Plan, sel: Selection, Q, K, V, O, dO, lse, grad
     named += _check_plan(p, pl) + _check_selection(p, sel, True)
     dev = _check_devices(named)
     lib = _lib.load()
-    with torch.cuda.device(dev):
+    made = out is None
+    with torch.cuda.device(dev), _alloc_on(stream, dev):
         if out is None:
             out = tuple(torch.empty(shape, dtype=dt, device=dev) for _ in range(3))
         ws = ws if ws is not None else _workspace(lib.prism_attn_workspace_size(C.byref(p), 1), dev)
@@ -403,6 +452,7 @@ def attn_bwd(p: PrismParams, pl: Plan, sel: Selection, Q, K, V, O, dO, lse, grad
                                  _ptr(O_res), _ptr(dO), _ptr(lse), _ptr(dQ), _ptr(dK), _ptr(dV),
                                  int(bool(grad_fp32)), int(bool(deterministic)), _ptr(ws), ws.numel(),
                                  _stream(stream, dev)))
+    _hand_over(stream, dev, *(out if made else ()))
     return dQ, dK, dV
 
 
@@ -420,10 +470,12 @@ def workspace_status(ws: torch.Tensor, stream=None) -> int:
 # kept short: no device switch where the tensors' device is current already, the
 # current stream by its raw handle, addresses as plain integers, sizes of new
 # tensors as separate arguments (0.7 us less than a tuple).
-_HERE = contextlib.nullcontext()
-
-
-def _on(dev):
+def _on(dev, stream):
+    if stream is not None:
+        both = contextlib.ExitStack()
+        both.enter_context(torch.cuda.device(dev))
+        both.enter_context(_alloc_on(stream, dev))
+        return both
     return _HERE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
@@ -495,10 +547,13 @@ def ckpt8_pack(x: torch.Tensor, out: Ckpt8 | None = None, stream=None) -> Ckpt8:
     n, width = x.shape
     named = [("x", x)] + (_check_ckpt8(out, "out", n, width) if out is not None else [])
     dev = _check_devices(named)
-    with _on(dev):
+    made = out is None
+    with _on(dev, stream):
         out = out if out is not None else alloc_ckpt8(n, width, dev)
         cs = out.c_struct()
         check(_lib.load().prism_ckpt8_pack(_addr(x), n, width, ld, C.byref(cs), _handle(stream, dev)))
+    if stream is not None and made:
+        _hand_over(stream, dev, out.codes, out.scales)
     return out
 
 
@@ -514,10 +569,13 @@ def ckpt8_unpack(c: Ckpt8, out: torch.Tensor | None = None, stream=None) -> torc
         ld = _check_rows(out, "out", (n, c.width))
         named.append(("out", out))
     dev = _check_devices(named)
-    with _on(dev):
+    made = out is None
+    with _on(dev, stream):
         out = out if out is not None else torch.empty(n, c.width, dtype=torch.bfloat16, device=dev)
         cs = c.c_struct()
         check(_lib.load().prism_ckpt8_unpack(C.byref(cs), n, c.width, _addr(out), ld, _handle(stream, dev)))
+    if stream is not None and made:
+        _hand_over(stream, dev, out)
     return out
 
 
@@ -593,7 +651,8 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
         _check_workspace(ws, "ws")
     dev = _check_devices(named)
     lib = _lib.load()
-    with _on(dev):
+    given = (Y, Z, ws)
+    with _on(dev, stream):
         Y = Y if Y is not None else torch.empty(n, cout, dtype=torch.bfloat16, device=dev)
         if Z is None and save is not None:
             Z = torch.empty_like(Y, memory_format=torch.contiguous_format) if save == "bf16" else \
@@ -605,6 +664,10 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
                                    Y.data_ptr(), ldy,
                                    _addr(Z) if save == "bf16" else None, C.byref(z8) if z8 is not None else None,
                                    ws.data_ptr(), ws.numel(), _handle(stream, dev)))
+    if stream is not None:
+        z = (Z.codes, Z.scales) if save == "ckpt8" else (Z,)
+        _hand_over(stream, dev, *((Y,) if given[0] is None else ()), *(z if given[1] is None else ()),
+                   *((ws,) if given[2] is None else ()))
     return LinearResult(Y, Z, ws)
 
 
@@ -678,7 +741,8 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
         named.append(("ws", ws))
     dev = _check_devices(named)
     lib = _lib.load()
-    with _on(dev):
+    given = (dX, dW, db, ws)
+    with _on(dev, stream):
         if want_x and dX is None:
             dX = torch.empty(n, cin, dtype=torch.bfloat16, device=dev)
         if want_w and dW is None:
@@ -693,4 +757,6 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
         check(lib.prism_linear_bwd(C.byref(l), dY.data_ptr(), lddy, None if x8 else _addr(X), ldx, cx, _addr(W),
                                    None if z8 else _addr(Z), ldz, cz, _addr(dX), _addr(dW), _addr(db),
                                    1 if grad_fp32 else 0, ws.data_ptr(), ws.numel(), _handle(stream, dev)))
+    if stream is not None:
+        _hand_over(stream, dev, *(t for g, t in zip(given, (dX, dW, db, ws)) if g is None))
     return LinearGrads(dX, dW, db, ws)
