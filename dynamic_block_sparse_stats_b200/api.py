@@ -512,6 +512,8 @@ def _check_ckpt8(c, name, n, width):
         raise TypeError(f"{name} must be an api.Ckpt8, got {type(c).__name__}")
     if c.width != width:
         raise ValueError(f"{name} holds {c.width} channels, the call needs {width}")
+    if width > 0x7fffffff:
+        raise ValueError(f"{name} has {width} channels; the library holds them in 32 bits")
     ld = (width + 127) // 128 * 128
     _check_tensor(c.codes, name + ".codes", torch.int8, (n, ld))
     _check_tensor(c.scales, name + ".scales", torch.uint8, (n, ld // 32))
@@ -530,6 +532,8 @@ def _check_rows(t, name, shape=None):
         want = "two dimensions" if shape is None else f"shape {tuple(shape)}"
         raise ValueError(f"{name} must have {want}, got {tuple(got)}")
     rows, cols = got
+    if cols > 0x7fffffff:
+        raise ValueError(f"{name} has {cols} channels; the library holds them in 32 bits")
     ld, step = t.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{name} rows must be contiguous")
@@ -603,12 +607,24 @@ class LinearGrads:
     ws: torch.Tensor
 
 
+def _describe(n, cin, cout, act) -> PrismLinear:
+    """The call's description.  What it holds in 32 bits is checked here: ctypes
+    would drop the upper ones, and the library see another size or activation."""
+    if not (-1 << 31 <= cin < 1 << 31 and -1 << 31 <= cout < 1 << 31):
+        raise ValueError(f"in and out are at most 65536 channels, got {cin}, {cout}")
+    if not ACT_NONE <= act <= ACT_GELU:
+        raise ValueError(f"act must be one of ACT_NONE .. ACT_GELU (0..3), got {act}")
+    if not -1 << 63 <= n < 1 << 63:
+        raise ValueError(f"n must be below 2^30 tokens, got {n}")
+    return PrismLinear(n, cin, cout, act)
+
+
 def linear_workspace_size(n: int, cin: int, cout: int, act: int = ACT_NONE, backward: bool = False,
                           x8: bool = False) -> int:
     """Bytes of the `ws` buffer linear_fwd / linear_bwd takes for n tokens (x8:
     linear_bwd with X as a Ckpt8)."""
     mode = (2 if x8 else 1) if backward else 0
-    size = _lib.load().prism_linear_workspace_size(C.byref(PrismLinear(n, cin, cout, act)), mode)
+    size = _lib.load().prism_linear_workspace_size(C.byref(_describe(n, cin, cout, act)), mode)
     if size == 0:
         raise _lib.PrismError(_lib.PRISM_ERR_INVALID_ARG, _lib.load().prism_last_error().decode(errors="replace"))
     return size
@@ -649,6 +665,7 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
             named += _check_ckpt8(Z, "Z", n, cout)
     if ws is not None:
         _check_workspace(ws, "ws")
+    l = _describe(n, cin, cout, act)
     dev = _check_devices(named)
     lib = _lib.load()
     given = (Y, Z, ws)
@@ -657,7 +674,6 @@ def linear_fwd(X: torch.Tensor, W: torch.Tensor, bias: torch.Tensor | None = Non
         if Z is None and save is not None:
             Z = torch.empty_like(Y, memory_format=torch.contiguous_format) if save == "bf16" else \
                 alloc_ckpt8(n, cout, dev)
-        l = PrismLinear(n, cin, cout, act)
         ws = ws if ws is not None else torch.empty(256, dtype=torch.uint8, device=dev)
         z8 = Z.c_struct() if save == "ckpt8" else None
         check(lib.prism_linear_fwd(C.byref(l), X.data_ptr(), ldx, W.data_ptr(), _addr(bias), _addr(residual), ldr,
@@ -739,6 +755,7 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
     if ws is not None:
         _check_workspace(ws, "ws")
         named.append(("ws", ws))
+    l = _describe(n, cin, cout, act)
     dev = _check_devices(named)
     lib = _lib.load()
     given = (dX, dW, db, ws)
@@ -749,7 +766,6 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
             dW = torch.empty(cout, cin, dtype=dt, device=dev)
         if want_b and db is None:
             db = torch.empty(cout, dtype=dt, device=dev)
-        l = PrismLinear(n, cin, cout, act)
         if ws is None:
             ws = _workspace(lib.prism_linear_workspace_size(C.byref(l), 2 if x8 else 1), dev)
         cx = C.byref(X.c_struct()) if x8 else None
