@@ -4,11 +4,11 @@
 //   code  x / 2^(s - 127) rounded to nearest, ties to even (|code| <= 127)
 // A code times its scale has at most 7 significant bits, so it is exact in
 // bf16 and the tensor cores multiply the stored values without a second
-// rounding; the rounding of the checkpoint itself is at most half a scale,
-// 2^-7 of the block's largest value (int8 with a power-of-two scale: about a
-// third of the error that an 8-bit float with 3 mantissa bits makes on normally
-// distributed values, whose error grows with the value).  A block that holds an
-// infinity or NaN gets s = 255 and codes 0, which restore as 0 * inf = NaN.
+// rounding; the rounding of the checkpoint itself is at most half a scale, less
+// than 1/127 of the block's largest value unless s = 1 (int8 with a power-of-two
+// scale: about a third of the error that an 8-bit float with 3 mantissa bits makes
+// on normally distributed values, whose error grows with the value).  A block that
+// holds an infinity or NaN gets s = 255 and codes 0, which restore as 0 * inf = NaN.
 // Finite values above 127 * 2^121 (the upper 0.4% of the last binade) are held
 // as that value: a larger scale could restore them as infinities.
 #pragma once

@@ -381,9 +381,10 @@ int prism_attn_bwd(const prism_params *p, const prism_plan_t *plan,
  * The value of a channel is code * 2^(s - 127), exact in bf16.  s is the
  * smallest integer >= 1 with max|x| <= 127 * 2^(s - 127) over the block, and
  * the code is x / 2^(s - 127) rounded to nearest, ties to even: each value is
- * off by at most half a scale, 2^-7 of the block's largest.  Values below 2^-127
- * become 0.  A block that holds an infinity or NaN has s = 255 and codes 0 and
- * stands for 32 NaNs; finite values above 127 * 2^121 are held as that value.
+ * off by at most half a scale, which is less than 1/127 of the block's largest
+ * unless s = 1 (blocks below 2^-119).  Values up to 2^-127 become 0.  A block
+ * that holds an infinity or NaN has s = 255 and codes 0 and stands for 32 NaNs;
+ * finite values above 127 * 2^121 are held as that value.
  */
 typedef struct prism_ckpt8_t {
   int8_t *codes;
