@@ -600,7 +600,9 @@ class LinearResult:
 @dataclass
 class LinearGrads:
     """Output of prism_linear_bwd: dX bf16 [n, in], dW [out, in], db [out]
-    (bf16 or fp32; None where not asked for), ws the call's workspace."""
+    (bf16 or fp32; None where not asked for), ws the call's workspace: its first
+    bytes are the status word, the rest dZ, partial sums and a restored X, of no
+    further use, which live as long as `ws` is held."""
     dX: torch.Tensor | None
     dW: torch.Tensor | None
     db: torch.Tensor | None
@@ -693,7 +695,9 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
     """prism_linear_bwd: the gradients named in `need` of linear_fwd, from dY
     bf16 [n, out], the forward's X [n, in] (bf16 or a Ckpt8; needed for dW), W
     (needed for dX) and, with an activation, the saved pre-activation Z (bf16 or
-    a Ckpt8).  dX is bf16; dW and db bf16, or fp32 with grad_fp32.  `out` may
+    a Ckpt8).  dX is bf16; dW and db bf16, or fp32 with grad_fp32 (with silu
+    or gelu, dW's operand dY * act'(Z) is rounded to bf16, and the fp32 dW is as
+    accurate as that: about 1.7e-3 of its norm; otherwise 5e-7).  `out` may
     hold (dX, dW, db) buffers, None entries allocated; the library refuses
     buffers that share memory with what the call reads (X's for dX unless `need`
     leaves dW out) or with one another.  The residual's gradient is dY itself."""

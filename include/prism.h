@@ -476,8 +476,11 @@ int prism_linear_fwd(const prism_linear_t *l, const uint16_t *X, int64_t ldx,
  *   dX      bf16 [n][in], or NULL.
  *   dW, db  [out][in] and [out], or NULL: bf16 when grad_fp32 == 0, fp32 else.
  * dZ is rounded to bf16 for the two products (the operand type of the tensor
- * cores, and of dY itself); db sums the fp32 values.  Every sum is held in
- * fp32 and taken in a fixed order: the outputs are bitwise reproducible.
+ * cores, and of dY itself); db sums the fp32 values.  So with silu or gelu an
+ * fp32 dW carries that rounding, up to 2^-8 of each token's share (about 1.7e-3
+ * of the norm); without an activation or with relu its operands are exact, and
+ * it is good to about 5e-7 of the norm.  Every sum is held in fp32 and taken in
+ * a fixed order: the outputs are bitwise reproducible.
  * With n = 0, dW and db are zero.
  * No output (dX, dW, db, the workspace) may share memory with what the call
  * reads (dY; X or X8 if dW is asked for; W if dX is; Z or Z8 with an

@@ -97,3 +97,25 @@ def test_gradients_along_themselves(n, cin, cout, act, z8, fp32):
             assert not held(bad, v)[0], name
         v = np.sign(exact[i]) * np.abs(rng.normal(size=exact[i].shape))
         assert held(got[i], v)[0] and not held(0 * got[i], v)[0] and not held(-got[i], v)[0], name
+
+
+@pytest.mark.parametrize("act", [api.ACT_NONE, api.ACT_RELU, api.ACT_SILU, api.ACT_GELU])
+def test_what_fp32_weight_gradients_are_good_to(act):
+    """Without an activation, and with relu, the operands are exact: 16 additions of 2^-23 of the sum
+    for the chains and their joining.  With one, dZ's rounding to bf16 is in it: 2^-8
+    / sqrt(3) of the norm in the mean square at most, and more than a hundredth of it
+    for dZ's values are not bf16's."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(act)
+    n, cin, cout = 20000, 264, 520
+    X, W, dY = (torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16) for s in ((n, cin), (cout, cin), (n, cout)))
+    Z = torch.randn(n, cout, generator=g, device="cuda").to(torch.bfloat16)
+    got = api.linear_bwd(dY, X, W, Z, act, need=("dW",), grad_fp32=True)
+    dZ = dY.double() * torch.from_numpy(L.slope(_np(Z), act)).cuda()
+    rel = lambda a, b: float((a.double() - b).norm() / b.norm())  # noqa: E731
+    dw = rel(got.dW, dZ.t() @ X.double())
+    rms = 2.0 ** -8 / 3 ** 0.5
+    if act <= api.ACT_RELU:                      # relu's slopes are 0 and 1
+        assert dw < 16 * STEP
+    else:
+        assert rms / 100 < dw < rms
