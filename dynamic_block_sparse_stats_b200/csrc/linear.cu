@@ -223,13 +223,28 @@ static cudaError_t launch_split(const Plan &p, const Maps &m, const Args &args, 
 
 // Whether a pair tile's epilogue gets 16 warps.  Eight are enough once the
 // products of a tile (kc stages) take longer than its epilogue; below that the
-// epilogue sets the time.  Measured at 92160 tokens, 8 against 16 warps (us):
-//   no activation     256 -> 256: 21.3, 18.8   512 -> 512: 44.5, 50.5
-//   bias, residual    512 -> 512: 63, 59       1024 -> 1024: 161, 176
-//   bias, gelu        768 -> 768: 104, 97      1024 -> 1024: 156, 161
-//   and Z saved       768 -> 768: 126, 114     1024 -> 1024: 186, 180
+// epilogue sets the time, and 16 hide one another's latencies, at the price of a
+// stage.  Measured with both from 2 to 48 stages, 46080 tokens -> 1024 channels and
+// 92160 -> 512 (us, the first, 8 warps and 16, around where they cross):
+//   bias                    6: 47.6, 41.1    7: 47.2, 46.0    8: 48.5, 49.2
+//   residual                8: 61.2, 56.1    9: 62.7, 63.1   10: 64.1, 66.7
+//   bias, gelu             12: 72.8, 66.2   14: 76.7, 74.6   16: 81.8, 83.2
+//   bias, Z in bf16        10: 69.8, 68.4   12: 75.5, 75.2   14: 79.8, 82.8
+//   the same with gelu     16: 97.4, 92.5   18: 102.8, 100.5 20: 108.0, 108.2
+//   bias, Z in 8 bits      12: 78.1, 72.7   14: 83.6, 80.9   16: 87.8, 89.1
+//   the same with gelu     18: 107.2, 100.4 20: 110.8, 108.2 22: 116.7, 116.3
+// A residual beside a saved Z moves the last by a stage or two.  Far beyond, 8 warps
+// win by 1 to 2% (48 stages, gelu and Z: 220, 222).  Two staging buffers a warp and
+// five stages, which this replaced, were ahead at 92160 x 512 -> 512 with a residual
+// alone (56.3 against 58.4) and by up to 4% with gelu and Z in 8 bits around 20 stages
+// (46080 x 1280 -> 1024: 104.2 against 107.4); level or behind, up to 30%, elsewhere.
 static bool wide_epilogue(const Args &a) {
-  const int enough = a.save_z ? 48 : a.act == PRISM_ACT_SILU || a.act == PRISM_ACT_GELU ? 14 : a.has_res ? 9 : 6;
+  const bool curved = a.act == PRISM_ACT_SILU || a.act == PRISM_ACT_GELU;  // an exponential and a reciprocal a value
+  const int enough = a.save_z == 2   ? (curved ? 22 : 15)
+                     : a.save_z == 1 ? (curved ? 19 : 13)
+                     : curved        ? 15
+                     : a.has_res     ? 9
+                                     : 7;
   return a.s.kc < enough;
 }
 
