@@ -17,11 +17,11 @@
 // power of two) in the swizzled layout the tensor cores read.
 //
 // SUM: the tensor cores add into their fp32 accumulator with truncation, an
-// error that grows with the length of the chain (measured: 7e-8 of the sum's
-// norm per 64 tokens, 2e-5 over the 20,000-token chains of a 92160-token weight
-// gradient).  An fp32 output therefore takes chains of kChain stages only; the
-// epilogue warps add each to rounded fp32 sums in registers, while the next
-// chain runs in the other accumulator.
+// error toward zero that grows with the length of the chain (measured a stage of
+// 64 tokens: 7e-8 of the norm for sums of random signs, 3.5e-7 for sums of one
+// sign).  An fp32 output therefore takes chains of kChain stages only, and a bf16
+// weight gradient none above kLongChain; the epilogue warps add each to rounded
+// fp32 sums in registers, while the next chain runs in the other accumulator.
 //
 // Roles (warps): 0 TMA producer, 1 MMA issuer (CTA 0 of a pair), 2 TMEM owner,
 // 3 producer of the codes (B8) or the bias gradient's last step, from 4 on the
@@ -51,12 +51,21 @@ constexpr int kStageBuf = 4096;  // an epilogue warp's staging buffer: 32 rows x
 // eight: 757 us at 92160 x 1024 x 4096, two of four 705, four of two 705).
 constexpr int kConvTeams = 2;
 constexpr int kConvTeam = 4;
-constexpr int kChain = 8;  // stages per accumulator chain when SUM: 5e-7 of the norm, 4% of the time
+constexpr int kChain = 8;  // stages per accumulator chain of fp32 outputs: 5e-7 of the norm, 4% of the time
+// ... of bf16 weight gradients, whose tokens have no bound (the other products' have:
+// 1024 stages, 3.5e-4 where a sum keeps its sign, against a rounding of up to 3.9e-3).
+// One chain over 860160 tokens was 5e-3 short on such sums; this length costs nothing
+// that could be measured.
+constexpr int kLongChain = 512;
 
-template <int CG_, int BN_, bool A_MN_, bool B_MN_, bool B8_ = false, bool SUM_ = false, int EW_ = 8>
+enum { SUM_NONE = 0, SUM_FP32 = 1, SUM_BF16 = 2 };  // by the output's type
+
+template <int CG_, int BN_, bool A_MN_, bool B_MN_, bool B8_ = false, int SUM_ = SUM_NONE, int EW_ = 8>
 struct Cfg {
   static constexpr int CG = CG_, BN = BN_;
-  static constexpr bool A_MN = A_MN_, B_MN = B_MN_, B8 = B8_, SUM = SUM_;
+  static constexpr bool A_MN = A_MN_, B_MN = B_MN_, B8 = B8_, SUM = SUM_ != SUM_NONE;
+  static constexpr bool SUM16 = SUM_ == SUM_BF16;
+  static constexpr int CHAIN = SUM16 ? kLongChain : kChain;
   static constexpr int BM = 128 * CG;
   static constexpr int BNC = BN / CG;  // columns of B a CTA loads
   static constexpr int A_BYTES = 128 * BK * 2;
@@ -610,8 +619,8 @@ __device__ __forceinline__ void epilogue_tile(const CUtensorMap &mapY, const CUt
 }
 
 // SUM: the chains of a segment added up in registers (a thread's row x its
-// warp's columns), then written in fp32: a whole tile to the output, a
-// partial one to its slot.
+// warp's columns), then written: a whole tile to the output in its type, a
+// partial one to its slot in fp32.
 template <class C>
 __device__ __forceinline__ void epilogue_sum(const CUtensorMap &mapY, const CUtensorMap &mapZ, const Args &args, Bars &bar,
                                              uint8_t *staging, uint32_t tmem, int group, int rank, int warp, int lane) {
@@ -628,7 +637,7 @@ __device__ __forceinline__ void epilogue_sum(const CUtensorMap &mapY, const CUte
     float sum[COLS];
 #pragma unroll
     for (int i = 0; i < COLS; ++i) sum[i] = 0.f;
-    for (int k0 = sg.k0; k0 < sg.k1; k0 += kChain, ++t) {
+    for (int k0 = sg.k0; k0 < sg.k1; k0 += C::CHAIN, ++t) {
       const int ab = t & 1;
       ok = __all_sync(0xffffffffu, mbar_wait(&bar.acc_full[ab], (t >> 1) & 1, args.status, 411));
       if (!ok) break;
@@ -648,6 +657,27 @@ __device__ __forceinline__ void epilogue_sum(const CUtensorMap &mapY, const CUte
     if (!ok) break;
     const int m0 = (sg.tile / s.tiles_n) * C::BM + rank * 128 + q4 * 32;
     const int n0 = (sg.tile % s.tiles_n) * C::BN + half * COLS;
+    if (C::SUM16 && sg.slot < 0) {
+      uint8_t *row = buf + lane * 128;
+#pragma unroll
+      for (int c = 0; c < COLS / 64; ++c) {
+        if (lane == 0) store_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float *v = sum + c * 64 + i * 8;
+          *reinterpret_cast<uint4 *>(row + ((i ^ (lane & 7)) << 4)) =
+              make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (m0 < args.rows && n0 + c * 64 < args.cols) store_2d(&mapY, buf, n0 + c * 64, m0);
+          store_commit();
+        }
+      }
+      continue;
+    }
 #pragma unroll
     for (int g = 0; g < COLS / 32; ++g) {
       if (lane == 0) store_wait_read<0>();
@@ -779,7 +809,7 @@ __global__ void __cluster_dims__(C::CG, 1, 1) __launch_bounds__(C::THREADS, 1)
       bool ok = true;
       while (ok && it.next(s, sg)) {
         for (int k0 = sg.k0; ok && k0 < sg.k1; ++t) {
-          const int k1 = C::SUM ? min(k0 + kChain, sg.k1) : sg.k1;
+          const int k1 = C::SUM ? min(k0 + C::CHAIN, sg.k1) : sg.k1;
           const int ab = t & 1;
           if (t >= 2 && !(ok = mbar_wait(&bar.acc_empty[ab], ((t >> 1) - 1) & 1, status, 404))) break;
           tc_fence_after();

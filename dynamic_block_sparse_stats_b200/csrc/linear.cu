@@ -253,7 +253,7 @@ static cudaError_t launch_plan(const Plan &p, const Maps &m, const Args &args, c
   if (p.split && p.swap) return launch_split<B_MN, A_MN, true>(p, m, args, st);
   if (p.split) return launch_split<A_MN, B_MN>(p, m, args, st);
   if (p.cg == 1) return launch<Cfg<1, 128, A_MN, B_MN>>(m, args, st);
-  if (wide_epilogue(args)) return launch<Cfg<2, 256, A_MN, B_MN, false, false, 16>>(m, args, st);
+  if (wide_epilogue(args)) return launch<Cfg<2, 256, A_MN, B_MN, false, gemm::SUM_NONE, 16>>(m, args, st);
   return launch<Cfg<2, 256, A_MN, B_MN>>(m, args, st);
 }
 
@@ -346,7 +346,8 @@ static cudaError_t input_grad(const prism_linear_t &l, const uint16_t *dZ, long 
 }
 
 static Plan grad_plan(const prism_linear_t &l, bool fp32) {
-  return make_plan(l.out, l.in, (int)((l.n + gemm::BK - 1) / gemm::BK), true, fp32 ? gemm::kChain : 1 << 30, false, false);
+  return make_plan(l.out, l.in, (int)((l.n + gemm::BK - 1) / gemm::BK), true, fp32 ? gemm::kChain : gemm::kLongChain, false,
+                   false);
 }
 static size_t grad_part_bytes(const Plan &p) {
   return p.s.rem ? sizeof(float) * (size_t)(p.s.groups + p.s.rem) * (128 * p.cg) * p.bn : 0;
@@ -357,6 +358,13 @@ static size_t grad_part_bytes(const Plan &p) {
 // 92160 x 1024 in long runs, converted against restored (us): out = 512, 135 and
 // 172; 1024, 251 and 268; 2048, 464 and 434.
 static bool grad_restores(const prism_linear_t &l, const Plan &p) { return p.split || p.cg == 1 || l.out >= 2048; }
+
+template <int CG, int BN, bool B8>
+static cudaError_t launch_sum(int sum, const Maps &m, const Args &a, cudaStream_t st) {
+  if (sum == gemm::SUM_FP32) return launch<Cfg<CG, BN, true, true, B8, gemm::SUM_FP32>>(m, a, st);
+  if (sum == gemm::SUM_BF16) return launch<Cfg<CG, BN, true, true, B8, gemm::SUM_BF16>>(m, a, st);
+  return launch<Cfg<CG, BN, true, true, B8>>(m, a, st);
+}
 
 // dW [out][in] = dZ^T X, summed over the tokens
 static cudaError_t weight_grad(const prism_linear_t &l, const uint16_t *dZ, long long ldd, const uint16_t *X,
@@ -391,6 +399,10 @@ static cudaError_t weight_grad(const prism_linear_t &l, const uint16_t *dZ, long
     a.out_fp32 = fp32;
     return launch_split<true, true>(p, m, a, st);
   }
+  // whole tiles walk kc stages; where there are none, no group walks more than km
+  const int sum = fp32                                                     ? gemm::SUM_FP32
+                  : (p.s.full ? p.s.kc : p.s.km) > gemm::kLongChain ? gemm::SUM_BF16
+                                                                    : gemm::SUM_NONE;
   if (fp32)
     e = make_map_2d(&m.y, MAP_F32, dW, l.in, l.out, l.in, 32, 32);
   else
@@ -404,13 +416,11 @@ static cudaError_t weight_grad(const prism_linear_t &l, const uint16_t *dZ, long
     a.b_scales = X8->scales;
     a.b_ld = X8->ld;
     a.k_total = (int)l.n;
-    e = fp32 ? launch<Cfg<2, 256, true, true, true, true>>(m, a, st) : launch<Cfg<2, 256, true, true, true, false>>(m, a, st);
+    e = launch_sum<2, 256, true>(sum, m, a, st);
   } else if (p.cg == 2) {
-    e = fp32 ? launch<Cfg<2, 256, true, true, false, true>>(m, a, st)
-             : launch<Cfg<2, 256, true, true, false, false>>(m, a, st);
+    e = launch_sum<2, 256, false>(sum, m, a, st);
   } else {
-    e = fp32 ? launch<Cfg<1, 128, true, true, false, true>>(m, a, st)
-             : launch<Cfg<1, 128, true, true, false, false>>(m, a, st);
+    e = launch_sum<1, 128, false>(sum, m, a, st);
   }
   if (e != cudaSuccess || !p.s.rem) return e;
   Helpers who = {};
