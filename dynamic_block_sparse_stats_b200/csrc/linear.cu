@@ -37,11 +37,14 @@ using gemm::Sched;
 //   single  128 x 128 tiles, persistent: 0.35 a stage (L2 bound), 4.2 around
 //   split   128 x 64 tiles, the contraction over up to 8 CTAs of a cluster: 0.33
 //           a stage, 5.0 (8 CTAs) to 8.1 (one) around, one tile per cluster
-// A wave of tiles takes no less than its epilogues: 1.6 (pairs) and 1.3 (single)
-// us, 2.6 and 2.8 with an activation, a residual or a saved Z ("heavy"), which also
-// adds 2.8, 1.8 and 0.3 behind the last tile.  The least estimate is taken; against
-// all three timed at 27 sizes from 1 x 1024 x 4096 to 92160 x 1024 x 1024, the choice
-// is within a tenth of the best.
+// A wave of tiles takes no less than its epilogues: 1.8 (pairs) and 1.6 (single)
+// us, 4.2 and 3.0 with an activation, a residual or a saved Z ("heavy"); the first
+// wave's products and the last one's epilogue (0.1, heavy 2.6 and 2.0) have nothing
+// beside them.  The least estimate is taken.  Against all three timed at 42 sizes from
+// 1 x 1024 -> 4096 to 92160 x 1024 -> 1024, in seven forms each
+// (profiles/linear_tile_choice.md): forward and dX within 3% of the best, dW within 15%,
+// but for a checkpointed X with few output channels (40000 x 1152 -> 128: 51.3 us for
+// 39.3), whose conversion on the way the estimate does not know.
 struct Plan {
   int cg, bn;  // tile: 128 * cg rows, bn columns
   int split;   // > 0: split_kernel with clusters of this size
@@ -93,10 +96,13 @@ static Plan make_plan(int rows, int cols, int kc, bool share, int chain, bool ma
     p.bn = big ? 256 : 128;
     p.s = make_sched(p.cg, p.bn, rows, cols, kc, share);
     const double waves = p.s.rem ? (double)p.s.full / p.s.groups : (double)((p.s.tiles + p.s.groups - 1) / p.s.groups);
-    const double epilogue = big ? (heavy ? 2.6 : 1.6) : (heavy ? 2.8 : 1.3);
-    p.us = (big ? 6.0 : 4.2) + (heavy ? (big ? 2.8 : 1.8) : 0.0) + waves * std::max(kc * (big ? 0.40 : 0.35), epilogue);
-    // the shared tiles, and the kernel that adds their parts
-    if (p.s.rem) p.us += p.s.km * (big ? 0.40 : 0.35) + 5.0 + 0.02 * p.s.groups / p.s.rem;
+    const double stage = big ? 0.40 : 0.35, products = kc * stage;
+    const double epilogue = big ? (heavy ? 4.2 : 1.8) : (heavy ? 3.0 : 1.6);
+    p.us = big ? 6.0 : 4.2;
+    if (p.s.rem)  // the shared tiles, and the kernel that adds their parts
+      p.us += waves * std::max(products, epilogue) + p.s.km * stage + 5.0 + 0.02 * p.s.groups / p.s.rem;
+    else
+      p.us += products + (waves - 1) * std::max(products, epilogue) + (heavy ? (big ? 2.6 : 2.0) : 0.1);
     if (p.us < best.us) best = p;
   }
   Plan p = {};
