@@ -600,13 +600,20 @@ class LinearResult:
 @dataclass
 class LinearGrads:
     """Output of prism_linear_bwd: dX bf16 [n, in], dW [out, in], db [out]
-    (bf16 or fp32; None where not asked for), ws the call's workspace: its first
-    bytes are the status word, the rest dZ, partial sums and a restored X, of no
-    further use, which live as long as `ws` is held."""
+    (bf16 or fp32; None where not asked for), ws the call's workspace, or a copy
+    of its header with the status word where the call allocated more than
+    _KEPT_WORKSPACE bytes: dZ, partial sums and a restored X are of no further
+    use."""
     dX: torch.Tensor | None
     dW: torch.Tensor | None
     db: torch.Tensor | None
     ws: torch.Tensor
+
+
+# A backward's workspace holds dZ and perhaps X, as large as the activations.  Above this
+# size it is given back with the call; the copy of its header takes 2 to 4 us, beside calls
+# of 100 us or more.
+_KEPT_WORKSPACE = 1 << 26
 
 
 def _describe(n, cin, cout, act) -> PrismLinear:
@@ -777,6 +784,8 @@ def linear_bwd(dY: torch.Tensor, X: torch.Tensor | Ckpt8 | None, W: torch.Tensor
         check(lib.prism_linear_bwd(C.byref(l), dY.data_ptr(), lddy, None if x8 else _addr(X), ldx, cx, _addr(W),
                                    None if z8 else _addr(Z), ldz, cz, _addr(dX), _addr(dW), _addr(db),
                                    1 if grad_fp32 else 0, ws.data_ptr(), ws.numel(), _handle(stream, dev)))
+        if given[3] is None and ws.numel() > _KEPT_WORKSPACE and (stream is None or isinstance(stream, torch.cuda.Stream)):
+            ws = ws[:256].clone()
     if stream is not None:
         _hand_over(stream, dev, *(t for g, t in zip(given, (dX, dW, db, ws)) if g is None))
     return LinearGrads(dX, dW, db, ws)

@@ -104,3 +104,47 @@ def test_outputs_beside_operands_in_one_buffer():
     place = X.clone()
     got = api.linear_bwd(dY, place, W, need=("dX", "db"), out=(place, None, None))
     assert got.dX is place and torch.equal(place, grads.dX) and torch.equal(got.db, grads.db)
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_a_large_workspace_is_given_back_with_the_call(own_stream):
+    """dZ, the partial sums and a restored X do not outlive the call; the status does."""
+    n, cin, cout = 20000, 264, 2056
+    g = _gen(8)
+    X, W, dY, Z = _rand(g, n, cin), _rand(g, cout, cin), _rand(g, n, cout), _rand(g, n, cout)
+    x8 = api.ckpt8_pack(X)
+    want = api.linear_bwd(dY, x8, W, Z, api.ACT_GELU,
+                          ws=torch.empty(api.linear_workspace_size(n, cin, cout, api.ACT_GELU, True, True), dtype=torch.uint8,
+                                         device="cuda"))
+    assert want.ws.numel() > 2 * n * cout
+    stream = torch.cuda.Stream() if own_stream else None
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    got = api.linear_bwd(dY, x8, W, Z, api.ACT_GELU, stream=stream)
+    held = torch.cuda.memory_allocated() - before
+    grads = sum(t.numel() * t.element_size() for t in (got.dX, got.dW, got.db))
+    # the allocator gives a tensor up to 1 MiB more than asked for (a block's rest below that is not
+    # split off): three gradients and the header; the workspace is 82 MB and more
+    assert held <= grads + (4 << 20)
+    torch.cuda.synchronize()
+    assert api.workspace_status(got.ws) == _lib.PRISM_OK
+    assert all(torch.equal(getattr(got, k), getattr(want, k)) for k in ("dX", "dW", "db"))
+    small = api.linear_bwd(dY[:500], X[:500], W, Z[:500], api.ACT_GELU)
+    assert small.ws.numel() > 256 and api.workspace_status(small.ws) == _lib.PRISM_OK
+
+
+def test_the_status_of_a_large_call_in_a_graph():
+    n, cin, cout = 20000, 264, 2056
+    g = _gen(9)
+    X, W, dY, Z = _rand(g, n, cin), _rand(g, cout, cin), _rand(g, n, cout), _rand(g, n, cout)
+    want = api.linear_bwd(dY, X, W, Z, api.ACT_SILU)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = api.linear_bwd(dY, X, W, Z, api.ACT_SILU)
+        later = torch.zeros(64 << 20, dtype=torch.uint8, device="cuda")    # may take the workspace's place
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert api.workspace_status(got.ws) == _lib.PRISM_OK and (later == 0).all()
+        assert all(torch.equal(getattr(got, k), getattr(want, k)) for k in ("dX", "dW", "db"))
