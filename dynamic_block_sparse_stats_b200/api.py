@@ -472,9 +472,10 @@ def workspace_status(ws: torch.Tensor, stream=None) -> int:
 # tensors as separate arguments (0.7 us less than a tuple).
 def _on(dev, stream):
     if stream is not None:
+        there = _alloc_on(stream, dev)  # may refuse the stream: before anything is entered
         both = contextlib.ExitStack()
         both.enter_context(torch.cuda.device(dev))
-        both.enter_context(_alloc_on(stream, dev))
+        both.enter_context(there)
         return both
     return _HERE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
