@@ -22,8 +22,10 @@ def entered(monkeypatch):
     @contextlib.contextmanager
     def device(d):
         now.append(d)
-        yield
-        now.remove(d)
+        try:
+            yield
+        finally:
+            now.remove(d)
 
     monkeypatch.setattr(torch.cuda, "Stream", _Stream)
     monkeypatch.setattr(torch.cuda, "device", device)
