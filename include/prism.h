@@ -512,7 +512,7 @@ uint64_t prism_kernel_launches(void);
 
 /* Optional timing of the attention path's kernels, for measurement (not meant
  * to be toggled by one thread while another launches through the library; the
- * linear maps and the checkpoints, one to four launches a call, carry none).  When
+ * linear maps and the checkpoints, one to six launches a call, carry none).  When
  * enabled, every kernel launch of the path is bracketed by a CUDA event pair
  * recorded on its launching stream.
  * prism_kernel_timing(1) clears the records and enables; (0) clears and
