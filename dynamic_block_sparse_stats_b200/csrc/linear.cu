@@ -36,7 +36,8 @@ using gemm::Sched;
 //           bound, 80% of the tensor pipe), 6.0 around them
 //   single  128 x 128 tiles, persistent: 0.35 a stage (L2 bound), 4.2 around
 //   split   128 x 64 tiles, the contraction over up to 8 CTAs of a cluster: 0.33
-//           a stage, 5.0 (8 CTAs) to 8.1 (one) around, one tile per cluster
+//           a stage, 5.0 (8 CTAs) to 8.1 (one) around, one tile per cluster; 0.3
+//           more with what is called heavy below
 // A wave of tiles takes no less than its epilogues: 1.8 (pairs) and 1.6 (single)
 // us, 4.2 and 3.0 with an activation, a residual or a saved Z ("heavy"); the first
 // wave's products and the last one's epilogue (0.1, heavy 2.6 and 2.0) have nothing

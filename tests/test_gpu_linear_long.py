@@ -53,3 +53,25 @@ def test_sums_of_one_sign(n, cin, cout):
             if x is x8:
                 same = api.linear_bwd(dY, api.ckpt8_unpack(x8), None, need=("dW",), grad_fp32=fp32)
                 assert torch.equal(same.dW, g.dW)
+
+
+@pytest.mark.parametrize("n,out", [(300, 64), (3000, 256), (9500, 512)])
+def test_the_longest_contraction_of_the_forward_and_of_dx(n, out):
+    """65536 channels, 1024 stages in one chain: 4096 instructions, 2^-10, and the
+    output's rounding, as above."""
+    wide = 65536
+    X, W = _positive(3, n, wide), _positive(4, out, wide)
+    tol = 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -16
+    rows = torch.cat([torch.arange(0, 64), torch.arange(n - 64, n)]).cuda()
+    want = X[rows].double() @ W.double().t()
+    for save in (None, "bf16"):
+        f = api.linear_fwd(X, W, save=save)
+        assert api.workspace_status(f.ws) == 0
+        for got in (f.Y, f.Z) if save else (f.Y,):
+            off = float(((got[rows].double() - want).abs() / want).max())
+            print(f"forward: {off / tol:.3f} of the tolerance")
+            assert off <= tol
+    # dX of a map to 65536 channels: the same product
+    g = api.linear_bwd(X, None, W.t().contiguous(), need=("dX",))
+    assert api.workspace_status(g.ws) == 0
+    assert float(((g.dX[rows].double() - want).abs() / want).max()) <= tol
